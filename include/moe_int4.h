@@ -259,6 +259,123 @@ int32_t moe_int8_linear(const uint16_t *x, const int32_t *w_packed, const uint16
                         int32_t tokens, int32_t n, int32_t k, int32_t group, uint16_t *out,
                         void *workspace, size_t workspace_bytes, void *hip_stream);
 
+/* Element types of the operands that come in more than one. */
+#define MOE_TYPE_BF16 0
+#define MOE_TYPE_F16 1
+#define MOE_TYPE_F32 2
+
+/* Activations of moe_int8_linear_fused. */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_RELU 1
+#define MOE_ACT_SILU 2       /* v / (1 + e^-v) */
+#define MOE_ACT_GELU 3       /* v Phi(v), by the complementary error function */
+#define MOE_ACT_GELU_TANH 4  /* v / (1 + e^-2u), u = sqrt(2/pi) (v + 0.044715 v^3) */
+#define MOE_ACT_SIGMOID 5    /* 1 / (1 + e^-v) */
+
+/* What moe_int8_linear_fused does to a row of products before its one store.
+ *   bias      [n] of bias_type, or NULL
+ *   residual  [tokens][n] of residual_type, rows residual_stride elements
+ *             apart, or NULL
+ *   activation  MOE_ACT_*
+ * A type is read only where its pointer is set. */
+typedef struct moe_int8_epilogue {
+    const void *bias;
+    const void *residual;
+    int64_t residual_stride;
+    int32_t bias_type;
+    int32_t residual_type;
+    int32_t activation;
+} moe_int8_epilogue;
+
+/* moe_int8_linear with bias, activation and residual in its epilogue (the
+ * hyper-connection's down projection is followed by a SiLU, its up projection
+ * by an addition to the residual stream: section 3.3, "Hyper-connection
+ * (decode-04)"), for rows that lie inside wider ones:
+ *   out[t][r] = residual[t][r] + act(sum_i x[t][i] * (byte[r][i] - 128)
+ *               * scale[r][i / group] + bias[r])
+ * in fp32, rounded once (to nearest even; a value beyond fp16's range becomes
+ * infinite) to out_type.
+ *   x    bf16 [tokens][k], rows x_stride elements apart: x_stride >= k, a
+ *        multiple of 8
+ *   out  [tokens][n] of out_type, rows out_stride >= n elements apart; what
+ *        lies between the rows is left as it was
+ *   epilogue  may be NULL (out is then the plain product)
+ * With one token the strides are not read.  x, w_packed and w_scales are
+ * 16-byte aligned; bias, residual and out need the alignment of their
+ * elements only.  out must not overlap x or bias; it may be the residual
+ * itself (same address, type and stride), and must not overlap it otherwise.
+ * Shapes, activations and determinism as in moe_int8_linear.  The workspace
+ * (moe_int8_linear_fused_workspace_bytes; NULL when that is 0) needs no
+ * clearing and holds nothing between calls; calls in flight at the same time
+ * need one each.  The stream must belong to the current device. */
+int32_t moe_int8_linear_fused_workspace_bytes(int32_t tokens, int32_t n, int32_t k, int32_t group,
+                                              size_t *bytes);
+int32_t moe_int8_linear_fused(const uint16_t *x, int64_t x_stride, const int32_t *w_packed,
+                              const uint16_t *w_scales, int32_t tokens, int32_t n, int32_t k,
+                              int32_t group, const moe_int8_epilogue *epilogue, void *out,
+                              int32_t out_type, int64_t out_stride, void *workspace,
+                              size_t workspace_bytes, void *hip_stream);
+
+/* Rules on the logits of a decoding step, row by row (a row is a sequence
+ * that asks for its next token).  Every pointer is device memory or NULL:
+ *   history  int32 [rows][history_width], rows history_stride elements apart:
+ *            row r's tokens so far are its first history_lengths[r] entries,
+ *            the first prompt_lengths[r] of them the prompt
+ *   history_lengths, prompt_lengths  int32 [rows] (NULL: every entry of the
+ *            row; no prompt), taken as clamped to [0, history_width]
+ *   repetition   fp32 [rows], > 0 (NULL: 1)
+ *   frequency, presence  fp32 [rows] (NULL: 0)
+ *   bias_ids int32, bias_values fp32 [rows][bias_width], rows bias_stride
+ *            elements apart; bias_lengths int32 [rows] (NULL: every entry),
+ *            clamped to [0, bias_width].  Of a token listed twice the last
+ *            entry holds.
+ *   temperature  fp32 [rows] (NULL: 1); a row whose temperature is not above
+ *            zero (greedy) is not scaled
+ *   mask     uint32 words, rows mask_stride words apart (0: one row for all):
+ *            bit v % 32 of word v / 32 is set where token v is allowed
+ * Ids outside [0, vocab) (padding) are ignored. */
+typedef struct moe_int4_logits_rules {
+    const int32_t *history;
+    const int32_t *history_lengths;
+    const int32_t *prompt_lengths;
+    const float *repetition;
+    const float *frequency;
+    const float *presence;
+    const int32_t *bias_ids;
+    const float *bias_values;
+    const int32_t *bias_lengths;
+    const float *temperature;
+    const uint32_t *mask;
+    int64_t history_stride;
+    int64_t bias_stride;
+    int64_t mask_stride;
+    int32_t history_width;
+    int32_t bias_width;
+} moe_int4_logits_rules;
+
+/* Applies the rules.  With c the count of token v behind the row's prompt:
+ *   l = logits[r][v]
+ *   v in the history:  l = l > 0 ? l / repetition : l * repetition
+ *   c > 0:             l = l - (frequency * c + presence)
+ *   v has a bias:      l = l + bias
+ *   temperature > 0:   l = l / temperature
+ *   mask bit clear:    l = -infinity, whatever l was (NaN too)
+ * in fp32, rounded once to out_type.  A row whose mask leaves nothing comes
+ * out as -infinity everywhere.
+ *   logits  [rows][vocab] of logits_type, rows logits_stride apart
+ *   out     [rows][vocab] of out_type, rows out_stride apart; what lies
+ *           between the rows is left as it was.  It may be the logits
+ *           themselves (same address, type and stride) and must not overlap
+ *           them otherwise, nor any of the rules' tables.
+ * rows in [0, 65536] (0 is a no-op), vocab in [1, 2^24], rows * vocab below
+ * 2^34, widths in [0, 2^24].
+ * Pointers need the alignment of their elements only.  Needs no workspace.
+ * The result does not depend on the order in which the history is counted.
+ * The stream must belong to the current device. */
+int32_t moe_int4_logits_process(const void *logits, int32_t logits_type, int64_t logits_stride,
+                           int32_t rows, int32_t vocab, const moe_int4_logits_rules *rules, void *out,
+                           int32_t out_type, int64_t out_stride, void *hip_stream);
+
 /* Message for the calling thread's most recent failing call ("" if none). */
 const char *moe_int4_last_error(void);
 

@@ -30,6 +30,19 @@ class MoeSharedInt6(ctypes.Structure):
                 ("inter", _c_i32), ("group", _c_i32)]
 
 
+class MoeInt8Epilogue(ctypes.Structure):
+    _fields_ = [("bias", _c_void_p), ("residual", _c_void_p), ("residual_stride", ctypes.c_int64),
+                ("bias_type", _c_i32), ("residual_type", _c_i32), ("activation", _c_i32)]
+
+
+class MoeLogitsRules(ctypes.Structure):
+    _fields_ = ([(f, _c_void_p) for f in ("history", "history_lengths", "prompt_lengths", "repetition",
+                                          "frequency", "presence", "bias_ids", "bias_values",
+                                          "bias_lengths", "temperature", "mask")]
+                + [(f, ctypes.c_int64) for f in ("history_stride", "bias_stride", "mask_stride")]
+                + [("history_width", _c_i32), ("bias_width", _c_i32)])
+
+
 class MoeError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"moe_int4 error {code}: {msg}")
@@ -56,11 +69,18 @@ def lib() -> ctypes.CDLL:
         L.moe_int4_quantize.argtypes = [P, _c_i32, _c_i32, _c_i32, P, P, P]
         L.moe_int8_linear_workspace_bytes.argtypes = [_c_i32] * 4 + [ctypes.POINTER(ctypes.c_size_t)]
         L.moe_int8_linear.argtypes = [P, P, P] + [_c_i32] * 4 + [P, P, ctypes.c_size_t, P]
+        c_i64 = ctypes.c_int64
+        L.moe_int8_linear_fused_workspace_bytes.argtypes = [_c_i32] * 4 + [ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_int8_linear_fused.argtypes = [P, c_i64, P, P] + [_c_i32] * 4 + [P, P, _c_i32, c_i64, P,
+                                                                             ctypes.c_size_t, P]
+        L.moe_int4_logits_process.argtypes = [P, _c_i32, c_i64, _c_i32, _c_i32, P, P, _c_i32, c_i64, P]
         L.moe_int4_last_error.restype = ctypes.c_char_p
         L.moe_int4_version.restype = ctypes.c_char_p
         for f in ("moe_int4_workspace_bytes", "moe_int4_route", "moe_int4_experts", "moe_int4_forward",
                   "moe_int4_forward_traced", "moe_int4_forward_noalloc", "moe_int4_quantize",
-                  "moe_int8_linear_workspace_bytes", "moe_int8_linear"):
+                  "moe_int8_linear_workspace_bytes", "moe_int8_linear",
+                  "moe_int8_linear_fused_workspace_bytes", "moe_int8_linear_fused",
+                  "moe_int4_logits_process"):
             getattr(L, f).restype = _c_i32
         _lib = L
     return _lib
@@ -70,6 +90,8 @@ EXPORTED = ("moe_int4_workspace_bytes", "moe_int4_route", "moe_int4_experts",
             "moe_int4_forward", "moe_int4_forward_traced", "moe_int4_forward_noalloc",
             "moe_int4_quantize",
             "moe_int8_linear_workspace_bytes", "moe_int8_linear",
+            "moe_int8_linear_fused_workspace_bytes", "moe_int8_linear_fused",
+            "moe_int4_logits_process",
             "moe_int4_last_error", "moe_int4_version")
 
 
@@ -207,6 +229,94 @@ def moe_int8_linear(x, w_packed, w_scales, tokens: int, n: int, k: int, group: i
     _check(lib().moe_int8_linear(_ptr(x), _ptr(w_packed), _ptr(w_scales), int(tokens), int(n), int(k),
                                  int(group), _ptr(out), _ptr(workspace),
                                  0 if workspace is None else workspace.numel(), _stream(stream)))
+
+
+# Element types (MOE_TYPE_*) and activations (MOE_ACT_*).
+TYPE_BF16, TYPE_F16, TYPE_F32 = 0, 1, 2
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "sigmoid": 5}
+_types = None
+
+
+def type_code(dtype) -> int:
+    """MOE_TYPE_* of a torch dtype (int16 and uint16 hold bf16 bit patterns)."""
+    global _types
+    if _types is None:
+        import torch
+        _types = {torch.bfloat16: TYPE_BF16, torch.int16: TYPE_BF16, torch.uint16: TYPE_BF16,
+                  torch.float16: TYPE_F16, torch.float32: TYPE_F32}
+    code = _types.get(dtype)
+    if code is None:
+        raise ValueError(f"{dtype} is none of bfloat16 (or its bits in int16, uint16), float16, float32")
+    return code
+
+
+def row_stride(t, name: str, rows: int, cols: int) -> int:
+    """The row stride of a matrix argument of `rows` x `cols`, its elements
+    consecutive in a row."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} is {tuple(t.shape)}, expected ({rows}, {cols})")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be consecutive")
+    return t.stride(0)
+
+
+def on_device(device, **tensors):
+    """Every tensor given lies on `device`, a GPU: the library dereferences
+    its address there."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be on the GPU, not on {device}")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def moe_int8_linear_fused_workspace_bytes(tokens: int, n: int, k: int, group: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check(lib().moe_int8_linear_fused_workspace_bytes(int(tokens), int(n), int(k), int(group), ctypes.byref(b)))
+    return b.value
+
+
+def moe_int8_linear_fused(x, w_packed, w_scales, tokens: int, n: int, k: int, group: int, out,
+                          bias=None, residual=None, activation: str = "none", workspace=None, stream=None):
+    """out [tokens, n] = residual + act(x W^T + bias): x bf16 [tokens, k],
+    w_packed int32 [n, k/4], w_scales bf16 [n, k/group], bias [n], residual
+    [tokens, n]; bias, residual and out in bf16, fp16 or fp32, the rows of x,
+    residual and out possibly inside wider ones.  activation: a key of
+    ACTIVATIONS.  workspace: uint8, may be None when the shape needs none."""
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation {activation!r} is none of {', '.join(ACTIVATIONS)}")
+    if type_code(x.dtype) != TYPE_BF16:
+        raise ValueError(f"x is {x.dtype}, expected bfloat16 (or its bits)")
+    xs, os_ = row_stride(x, "x", tokens, k), row_stride(out, "out", tokens, n)
+    out_type = type_code(out.dtype)
+    e = MoeInt8Epilogue(activation=ACTIVATIONS[activation])
+    if bias is not None:
+        if bias.dim() != 1 or bias.shape[0] != n or (n > 1 and bias.stride(0) != 1):
+            raise ValueError(f"bias is {tuple(bias.shape)}, expected ({n},), contiguous")
+        e.bias, e.bias_type = bias.data_ptr(), type_code(bias.dtype)
+    if residual is not None:
+        e.residual_stride = row_stride(residual, "residual", tokens, n)
+        e.residual, e.residual_type = residual.data_ptr(), type_code(residual.dtype)
+    on_device(x.device, w_packed=w_packed, w_scales=w_scales, out=out, bias=bias, residual=residual,
+              workspace=workspace)
+    _check(lib().moe_int8_linear_fused(x.data_ptr(), xs, w_packed.data_ptr(), w_scales.data_ptr(), tokens, n, k,
+                                       group, ctypes.byref(e), out.data_ptr(), out_type, os_, _ptr(workspace),
+                                       0 if workspace is None else workspace.numel(), _stream(stream)))
+
+
+def moe_int4_logits_process(logits, rules: MoeLogitsRules, out, stream=None):
+    """out = the rules applied to logits (both [rows, vocab] in bf16, fp16 or
+    fp32, rows possibly inside wider ones; out may be logits).  rules: device
+    addresses of the tables, which the caller keeps alive (layer.LogitsRules
+    does, and checks their shapes)."""
+    if logits.dim() != 2:
+        raise ValueError(f"logits is {tuple(logits.shape)}, expected [rows, vocab]")
+    rows, vocab = logits.shape
+    ls, os_ = row_stride(logits, "logits", rows, vocab), row_stride(out, "out", rows, vocab)
+    on_device(logits.device, out=out)
+    _check(lib().moe_int4_logits_process(logits.data_ptr(), type_code(logits.dtype), ls, rows, vocab,
+                                         ctypes.byref(rules), out.data_ptr(), type_code(out.dtype), os_,
+                                         _stream(stream)))
 
 
 def version() -> str:

@@ -225,6 +225,10 @@ int32_t check_int8_shape(int32_t tokens, int32_t n, int32_t k, int32_t group)
 
 size_t workspace_size(const Dims &d) { return layout(d).total; }
 
+static_assert(kBf16 == MOE_TYPE_BF16 && kF16 == MOE_TYPE_F16 && kF32 == MOE_TYPE_F32, "element types");
+static_assert(kActNone == MOE_ACT_NONE && kActRelu == MOE_ACT_RELU && kActSilu == MOE_ACT_SILU &&
+                  kActGelu == MOE_ACT_GELU && kActGeluTanh == MOE_ACT_GELU_TANH && kActSigmoid == MOE_ACT_SIGMOID,
+              "activations");
 static_assert(kKeysBytes == MOE_INT4_WS_STATUS_OFFSET, "status word follows the router keys");
 static_assert(kKeysBytes + kCtrlBytes == MOE_INT4_WS_PREFIX_BYTES, "control prefix size");
 static_assert(kStatusKeyWait == MOE_INT4_STATUS_KEY_WAIT && kStatusRouteWait == MOE_INT4_STATUS_ROUTE_WAIT &&
@@ -573,6 +577,216 @@ int32_t moe_int8_linear(const uint16_t *x, const int32_t *w_packed, const uint16
     return launched(launch_int8_linear(x, w_packed, w_scales, tokens, n, k, group, out, workspace,
                                        (hipStream_t)hip_stream),
                     "int8 linear");
+}
+
+// ---- typed and strided operands of the fused linear layer and of the rules on logits ----
+
+static bool known_type(int32_t t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_F16 || t == MOE_TYPE_F32; }
+
+// A matrix in device memory as the caller gave it.
+struct Rows {
+    const char *name;
+    const void *p;
+    int32_t type;
+    int64_t stride;   // elements between rows
+    int64_t rows, cols;
+};
+
+// Pointer, type, alignment and stride of one operand (one row: the stride is
+// not read).  Rows of up to 2^31 elements, 2^40 apart, keep every byte
+// offset far inside 63 bits.
+static int32_t check_rows(const Rows &m)
+{
+    if (!m.p) return fail(MOE_INT4_EINVAL, "%s is NULL", m.name);
+    if (!known_type(m.type)) return fail(MOE_INT4_EINVAL, "%s: type %d is none of MOE_TYPE_*", m.name, m.type);
+    if ((uintptr_t)m.p % (uintptr_t)type_bytes(m.type))
+        return fail(MOE_INT4_EALIGN, "%s is not aligned to its elements", m.name);
+    if (m.rows > 1 && (m.stride < m.cols || m.stride > ((int64_t)1 << 40)))
+        return fail(MOE_INT4_EINVAL, "%s: stride %lld outside [%lld, 2^40]", m.name, (long long)m.stride,
+                    (long long)m.cols);
+    return MOE_INT4_OK;
+}
+
+static uintptr_t row_bytes(const Rows &m) { return (uintptr_t)m.cols * type_bytes(m.type); }
+static uintptr_t pitch_bytes(const Rows &m) { return m.rows > 1 ? (uintptr_t)m.stride * type_bytes(m.type) : 0; }
+
+// Whether two operands may share bytes.  Exact where their rows are equally
+// far apart (column ranges of one wider matrix share none); otherwise their
+// whole extents decide.
+static bool may_overlap(const Rows &a, const Rows &b)
+{
+    const uintptr_t a0 = (uintptr_t)a.p, a1 = a0 + (a.rows - 1) * pitch_bytes(a) + row_bytes(a);
+    const uintptr_t b0 = (uintptr_t)b.p, b1 = b0 + (b.rows - 1) * pitch_bytes(b) + row_bytes(b);
+    if (a1 <= b0 || b1 <= a0) return false;
+    const uintptr_t pitch = pitch_bytes(a);
+    if (pitch && pitch == pitch_bytes(b)) {
+        const uintptr_t d = b0 >= a0 ? (b0 - a0) % pitch : (pitch - (a0 - b0) % pitch) % pitch;
+        return d < row_bytes(a) || d + row_bytes(b) > pitch;
+    }
+    return true;
+}
+
+static bool same_rows(const Rows &a, const Rows &b)
+{
+    return a.p == b.p && a.type == b.type && (a.rows <= 1 || a.stride == b.stride);
+}
+
+// Whether four elements at a multiple of four of every row are aligned.
+static bool rows_aligned4(const Rows &m)
+{
+    return (uintptr_t)m.p % (4u * type_bytes(m.type)) == 0 && (m.rows <= 1 || m.stride % 4 == 0);
+}
+
+static int32_t check_stream(hipStream_t st)
+{
+    if (!st) return MOE_INT4_OK;
+    int dev = -1, sdev = -1;
+    if (hipGetDevice(&dev) != hipSuccess) return fail(MOE_INT4_EDEVICE, "no HIP device is current");
+    if (hipStreamGetDevice(st, &sdev) != hipSuccess)
+        return fail(MOE_INT4_EINVAL, "hipStreamGetDevice failed for the given stream");
+    if (sdev != dev)
+        return fail(MOE_INT4_EINVAL, "the stream belongs to device %d, the current device is %d", sdev, dev);
+    return MOE_INT4_OK;
+}
+
+int32_t moe_int8_linear_fused_workspace_bytes(int32_t tokens, int32_t n, int32_t k, int32_t group,
+                                              size_t *bytes)
+{
+    g_error.clear();
+    int32_t rc = check_int8_shape(tokens, n, k, group);
+    if (rc) return rc;
+    if (!bytes) return fail(MOE_INT4_EINVAL, "bytes is NULL");
+    *bytes = int8_fused_plan(tokens, n, k, group).part_bytes;
+    return MOE_INT4_OK;
+}
+
+int32_t moe_int8_linear_fused(const uint16_t *x, int64_t x_stride, const int32_t *w_packed,
+                              const uint16_t *w_scales, int32_t tokens, int32_t n, int32_t k,
+                              int32_t group, const moe_int8_epilogue *epilogue, void *out,
+                              int32_t out_type, int64_t out_stride, void *workspace,
+                              size_t workspace_bytes, void *hip_stream)
+{
+    g_error.clear();
+    int32_t rc = check_int8_shape(tokens, n, k, group);
+    if (rc) return rc;
+    const moe_int8_epilogue none = {};
+    const moe_int8_epilogue &e = epilogue ? *epilogue : none;
+    if (e.activation < MOE_ACT_NONE || e.activation > MOE_ACT_SIGMOID)
+        return fail(MOE_INT4_EINVAL, "activation %d is none of MOE_ACT_*", e.activation);
+    if (tokens == 0) return MOE_INT4_OK;
+    if ((rc = check_ptrs({{"x", x}, {"w_packed", w_packed}, {"w_scales", w_scales}}))) return rc;
+    const Rows rx{"x", x, MOE_TYPE_BF16, x_stride, tokens, k};
+    const Rows ro{"out", out, out_type, out_stride, tokens, n};
+    const Rows rb{"bias", e.bias, e.bias_type, n, 1, n};
+    const Rows rr{"residual", e.residual, e.residual_type, e.residual_stride, tokens, n};
+    if ((rc = check_rows(rx)) || (rc = check_rows(ro))) return rc;
+    if (tokens > 1 && x_stride % 8)
+        return fail(MOE_INT4_EALIGN, "x: stride %lld is not a multiple of 8", (long long)x_stride);
+    if (may_overlap(rx, ro)) return fail(MOE_INT4_EINVAL, "out overlaps x");
+    bool vec = n % 4 == 0 && rows_aligned4(ro);
+    if (e.bias) {
+        if ((rc = check_rows(rb))) return rc;
+        if (may_overlap(rb, ro)) return fail(MOE_INT4_EINVAL, "out overlaps bias");
+        vec = vec && rows_aligned4(rb);
+    }
+    if (e.residual) {
+        if ((rc = check_rows(rr))) return rc;
+        if (!same_rows(rr, ro) && may_overlap(rr, ro))
+            return fail(MOE_INT4_EINVAL, "out overlaps residual without being the same rows");
+        vec = vec && rows_aligned4(rr);
+    }
+    const size_t need = int8_fused_plan(tokens, n, k, group).part_bytes;
+    if (need) {
+        if (!workspace) return fail(MOE_INT4_EINVAL, "workspace is NULL (%zu bytes needed)", need);
+        if (!aligned16(workspace)) return fail(MOE_INT4_EALIGN, "workspace is not 16-byte aligned");
+        if (workspace_bytes < need)
+            return fail(MOE_INT4_EWORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+    }
+    if ((rc = check_device()) || (rc = check_stream((hipStream_t)hip_stream))) return rc;
+    const Int8Epilogue d{e.bias, e.residual, out, tokens > 1 ? (size_t)x_stride : 0,
+                         tokens > 1 ? (size_t)e.residual_stride : 0, tokens > 1 ? (size_t)out_stride : 0,
+                         e.bias_type, e.residual_type, out_type, e.activation, vec};
+    return launched(launch_int8_linear_fused(x, w_packed, w_scales, tokens, n, k, group, d, workspace,
+                                             (hipStream_t)hip_stream),
+                    "int8 linear (fused)");
+}
+
+int32_t moe_int4_logits_process(const void *logits, int32_t logits_type, int64_t logits_stride,
+                                int32_t rows, int32_t vocab, const moe_int4_logits_rules *rules, void *out,
+                                int32_t out_type, int64_t out_stride, void *hip_stream)
+{
+    g_error.clear();
+    constexpr int kMost = 1 << 24;
+    if (rows < 0 || rows > (1 << 16)) return fail(MOE_INT4_EINVAL, "rows=%d outside [0, 65536]", rows);
+    if (vocab < 1 || vocab > kMost) return fail(MOE_INT4_EINVAL, "vocab=%d outside [1, 16777216]", vocab);
+    // at most 2^21 + 2^16 slabs of 8192: fewer than 2^32 threads in one launch
+    if ((int64_t)rows * vocab >= ((int64_t)1 << 34))
+        return fail(MOE_INT4_EINVAL, "rows * vocab = %lld must stay below 2^34", (long long)rows * vocab);
+    if (!rules) return fail(MOE_INT4_EINVAL, "rules is NULL");
+    const moe_int4_logits_rules &u = *rules;
+    if (u.history_width < 0 || u.history_width > kMost)
+        return fail(MOE_INT4_EINVAL, "history_width=%d outside [0, 16777216]", u.history_width);
+    if (u.bias_width < 0 || u.bias_width > kMost)
+        return fail(MOE_INT4_EINVAL, "bias_width=%d outside [0, 16777216]", u.bias_width);
+    if (rows == 0) return MOE_INT4_OK;
+    const Rows rl{"logits", logits, logits_type, logits_stride, rows, vocab};
+    const Rows ro{"out", out, out_type, out_stride, rows, vocab};
+    int32_t rc;
+    if ((rc = check_rows(rl)) || (rc = check_rows(ro))) return rc;
+    if (!same_rows(rl, ro) && may_overlap(rl, ro))
+        return fail(MOE_INT4_EINVAL, "out overlaps logits without being the same rows");
+    // the tables hold 4-byte words throughout: the fp32 type stands for all
+    const int64_t words = (vocab + 31) / 32;
+    const Rows tables[] = {
+        {"history", u.history, MOE_TYPE_F32, u.history_stride, rows, u.history_width},
+        {"bias_ids", u.bias_ids, MOE_TYPE_F32, u.bias_stride, rows, u.bias_width},
+        {"bias_values", u.bias_values, MOE_TYPE_F32, u.bias_stride, rows, u.bias_width},
+        {"mask", u.mask, MOE_TYPE_F32, u.mask_stride ? u.mask_stride : words, u.mask_stride ? rows : 1, words},
+        {"history_lengths", u.history_lengths, MOE_TYPE_F32, rows, 1, rows},
+        {"prompt_lengths", u.prompt_lengths, MOE_TYPE_F32, rows, 1, rows},
+        {"bias_lengths", u.bias_lengths, MOE_TYPE_F32, rows, 1, rows},
+        {"repetition", u.repetition, MOE_TYPE_F32, rows, 1, rows},
+        {"frequency", u.frequency, MOE_TYPE_F32, rows, 1, rows},
+        {"presence", u.presence, MOE_TYPE_F32, rows, 1, rows},
+        {"temperature", u.temperature, MOE_TYPE_F32, rows, 1, rows},
+    };
+    const bool history = u.history && u.history_width, biases = u.bias_ids && u.bias_width;
+    if (biases && !u.bias_values) return fail(MOE_INT4_EINVAL, "bias_values is NULL");
+    if (u.bias_values && u.bias_width && !u.bias_ids) return fail(MOE_INT4_EINVAL, "bias_ids is NULL");
+    for (const Rows &t : tables) {
+        if (!t.p || !t.cols) continue;
+        if ((rc = check_rows(t))) return rc;
+        if (may_overlap(t, ro)) return fail(MOE_INT4_EINVAL, "out overlaps %s", t.name);
+    }
+    if ((rc = check_device()) || (rc = check_stream((hipStream_t)hip_stream))) return rc;
+    LogitsArgs a{};
+    a.logits = logits;
+    a.out = out;
+    a.rows = rows;
+    a.vocab = vocab;
+    a.logits_stride = rows > 1 ? (size_t)logits_stride : 0;
+    a.out_stride = rows > 1 ? (size_t)out_stride : 0;
+    if (history) {
+        a.history = u.history;
+        a.history_stride = rows > 1 ? (size_t)u.history_stride : 0;
+        a.history_width = u.history_width;
+        a.history_lengths = u.history_lengths;
+        a.prompt_lengths = u.prompt_lengths;
+        a.repetition = u.repetition;
+        a.frequency = u.frequency;
+        a.presence = u.presence;
+    }
+    if (biases) {
+        a.bias_ids = u.bias_ids;
+        a.bias_values = u.bias_values;
+        a.bias_lengths = u.bias_lengths;
+        a.bias_stride = rows > 1 ? (size_t)u.bias_stride : 0;
+        a.bias_width = u.bias_width;
+    }
+    a.temperature = u.temperature;
+    a.mask = u.mask;
+    a.mask_stride = rows > 1 ? (size_t)u.mask_stride : 0;
+    return launched(launch_logits(a, logits_type, out_type, (hipStream_t)hip_stream), "logits");
 }
 
 }  // extern "C"

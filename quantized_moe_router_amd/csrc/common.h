@@ -529,4 +529,83 @@ Int8Plan int8_plan(int T, int N, int K, int G);
 hipError_t launch_int8_linear(const uint16_t *x, const int32_t *wq, const uint16_t *ws, int T, int N,
                               int K, int G, uint16_t *out, void *workspace, hipStream_t st);
 
+
+// Activations, as in the public header.
+constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4, kActSigmoid = 5;
+
+// Fused variant: what becomes of a row of sums before its store.
+struct Int8Epilogue {
+    const void *bias;       // [N] of bias_type, may be null
+    const void *residual;   // [T][N] of residual_type, may be null
+    void *out;              // [T][N] of out_type
+    size_t x_stride, residual_stride, out_stride;   // elements
+    int bias_type, residual_type, out_type, activation;
+    bool vec;               // every four columns at a multiple of four are aligned in bias, residual and out
+};
+Int8Plan int8_fused_plan(int T, int N, int K, int G);
+hipError_t launch_int8_linear_fused(const uint16_t *x, const int32_t *wq, const uint16_t *ws, int T, int N,
+                                    int K, int G, const Int8Epilogue &e, void *workspace, hipStream_t st);
+
+// Element types, as in the public header.
+constexpr int kBf16 = 0, kF16 = 1, kF32 = 2;
+__host__ __device__ inline int type_bytes(int type) { return type == kF32 ? 4 : 2; }
+
+// One element of a typed row as fp32, and back (to nearest even, once).
+__device__ __forceinline__ float load_typed(const void *p, int type, size_t i)
+{
+    if (type == kF32) return static_cast<const float *>(p)[i];
+    const uint16_t b = static_cast<const uint16_t *>(p)[i];
+    return type == kBf16 ? bf16_to_f32(b) : (float)__builtin_bit_cast(_Float16, b);
+}
+__device__ __forceinline__ void store_typed(void *p, int type, size_t i, float v)
+{
+    if (type == kF32)
+        static_cast<float *>(p)[i] = v;
+    else
+        static_cast<uint16_t *>(p)[i] =
+            type == kBf16 ? (uint16_t)f32_to_bf16(v) : __builtin_bit_cast(uint16_t, (_Float16)v);
+}
+// Four consecutive elements, aligned to the four.
+__device__ __forceinline__ float4 load_typed4(const void *p, int type, size_t i)
+{
+    if (type == kF32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+    const uint2 b = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+    if (type == kBf16) return make_float4(bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y));
+    const f16x2_t lo = __builtin_bit_cast(f16x2_t, b.x), hi = __builtin_bit_cast(f16x2_t, b.y);
+    return make_float4((float)lo[0], (float)lo[1], (float)hi[0], (float)hi[1]);
+}
+__device__ __forceinline__ void store_typed4(void *p, int type, size_t i, float4 v)
+{
+    if (type == kF32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = v;
+        return;
+    }
+    uint2 b;
+    if (type == kBf16) {
+        b = make_uint2(f32x2_to_bf16x2(v.x, v.y), f32x2_to_bf16x2(v.z, v.w));
+    } else {
+        const f16x2_t lo = {(_Float16)v.x, (_Float16)v.y}, hi = {(_Float16)v.z, (_Float16)v.w};
+        b = make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+    }
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i) = b;
+}
+
+// ---------------------------------------------------------------------------
+// Rules on logits (logits.hip)
+// ---------------------------------------------------------------------------
+struct LogitsArgs {
+    const void *logits;
+    void *out;
+    size_t logits_stride, out_stride;   // elements
+    int rows, vocab;
+    const int32_t *history, *history_lengths, *prompt_lengths;
+    const float *repetition, *frequency, *presence;
+    const int32_t *bias_ids, *bias_lengths;
+    const float *bias_values, *temperature;
+    const uint32_t *mask;
+    size_t history_stride, bias_stride, mask_stride;
+    int history_width, bias_width;   // 0: none
+};
+hipError_t launch_logits(const LogitsArgs &a, int in_type, int out_type, hipStream_t st);
+
 }  // namespace moe

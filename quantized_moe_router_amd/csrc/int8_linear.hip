@@ -78,6 +78,54 @@ __device__ __forceinline__ u32x4_t bf16x8_to_f16x8(u32x4_t v)
     return o;
 }
 
+// ---------------------------------------------------------------------------
+// Epilogue of the fused variant (F = true in the kernels below):
+//   out[t][r] = rnd(residual[t][r] + act(sum + bias[r]))
+// in fp32, one rounding.  Everything happens on the sum in registers, so the
+// activation and the addition cost no pass over [T][N] of their own.
+// exp, erfc and the division are the accurate ones: an fp32 output shows
+// errors that a bf16 one would hide.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float activate(float v, int kind)
+{
+    switch (kind) {   // uniform over the launch
+    case kActRelu: return v < 0.f ? 0.f : v;   // a NaN passes
+    case kActSilu: return v / (1.f + expf(-v));
+    case kActGelu: return 0.5f * v * erfcf(-0.70710678118654752f * v);
+    case kActGeluTanh: {
+        // 0.5 (1 + tanh u) = 1 / (1 + e^-2u), without tanh's cancellation near -1
+        const float u = 0.79788456080286536f * fmaf(0.044715f * v * v, v, v);
+        return v / (1.f + expf(-2.f * u));
+    }
+    case kActSigmoid: return 1.f / (1.f + expf(-v));
+    default: return v;
+    }
+}
+
+__device__ __forceinline__ void finish(const Int8Epilogue &e, int t, int r, float v)
+{
+    if (e.bias) v += load_typed(e.bias, e.bias_type, r);
+    v = activate(v, e.activation);
+    if (e.residual) v += load_typed(e.residual, e.residual_type, t * e.residual_stride + r);
+    store_typed(e.out, e.out_type, t * e.out_stride + r, v);
+}
+
+// Columns r .. r + 3 of one row (r a multiple of 4, e.vec set).
+__device__ __forceinline__ void finish4(const Int8Epilogue &e, int t, int r, float4 v)
+{
+    if (e.bias) {
+        const float4 b = load_typed4(e.bias, e.bias_type, r);
+        v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+    }
+    v = make_float4(activate(v.x, e.activation), activate(v.y, e.activation), activate(v.z, e.activation),
+                    activate(v.w, e.activation));
+    if (e.residual) {
+        const float4 b = load_typed4(e.residual, e.residual_type, t * e.residual_stride + r);
+        v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+    }
+    store_typed4(e.out, e.out_type, t * e.out_stride + r, v);
+}
+
 __device__ __forceinline__ float xor_shfl(float v, int m) { return __shfl_xor(v, m, 64); }
 
 // ---------------------------------------------------------------------------
@@ -119,13 +167,14 @@ __device__ __forceinline__ float wave_transpose_sum(float (&v)[M], int lane)
     return s;
 }
 
-template <int T>
+template <int T, bool F>
 __global__ __launch_bounds__(kGvThreads) void int8_gemv_kernel(const uint16_t *__restrict__ x,
                                                                const int32_t *__restrict__ wq,
                                                                const uint16_t *__restrict__ wscale,
                                                                int N, int K, int gshift,
-                                                               uint16_t *__restrict__ out)
+                                                               uint16_t *__restrict__ out, Int8Epilogue e)
 {
+    const size_t xstride = F ? e.x_stride : (size_t)K;
     // x as fp16 in LDS: chunk c (16 inputs) of token t is split into two
     // planes of 8 inputs, [t][p][c], so the 16-byte reads of consecutive
     // lanes are consecutive (no bank conflicts)
@@ -136,7 +185,7 @@ __global__ __launch_bounds__(kGvThreads) void int8_gemv_kernel(const uint16_t *_
     float *s_xsum = reinterpret_cast<float *>(s_x + T * 2 * CPR);
     for (int i = threadIdx.x; i < T * CPR; i += kGvThreads) {
         const int t = i / CPR, c = i - t * CPR;
-        const u32x4_t *src = reinterpret_cast<const u32x4_t *>(x + (size_t)t * K + 16 * c);
+        const u32x4_t *src = reinterpret_cast<const u32x4_t *>(x + t * xstride + 16 * c);
         const h2_t one = {(_Float16)1.f, (_Float16)1.f};
         float sum = 0.f;
 #pragma unroll
@@ -212,8 +261,8 @@ __global__ __launch_bounds__(kGvThreads) void int8_gemv_kernel(const uint16_t *_
             h2_t cp[8];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                cp[2 * q] = code_pair_biased<0>(r.w[j][q]);
-                cp[2 * q + 1] = code_pair_biased<1>(r.w[j][q]);
+                cp[2 * q] = F ? code_pair<0>(r.w[j][q]) : code_pair_biased<0>(r.w[j][q]);
+                cp[2 * q + 1] = F ? code_pair<1>(r.w[j][q]) : code_pair_biased<1>(r.w[j][q]);
             }
             const float sf = valid ? bf16_to_f32(r.s[j]) : 0.f;
 #pragma unroll
@@ -222,7 +271,7 @@ __global__ __launch_bounds__(kGvThreads) void int8_gemv_kernel(const uint16_t *_
 #pragma unroll
                 for (int q = 0; q < 8; ++q) p = __builtin_amdgcn_fdot2(cp[q], xv[t][q], p, false);
                 // sum (1024 + q) x - 1152 sum x = sum (q - 128) x
-                acc[j * T + t] = fmaf(sf, fmaf(-1152.f, xsum[t], p), acc[j * T + t]);
+                acc[j * T + t] = fmaf(sf, F ? p : fmaf(-1152.f, xsum[t], p), acc[j * T + t]);
             }
         }
         if (i == NI - 1) {
@@ -232,8 +281,10 @@ __global__ __launch_bounds__(kGvThreads) void int8_gemv_kernel(const uint16_t *_
             const int idx = lane >> shift;
             const int j = idx / T, t = idx - j * T;
             const int row = (gw + b * W) * kGvRows + j;
-            if ((lane & ((1 << shift) - 1)) == 0 && idx < kGvRows * T && row < N)
-                out[(size_t)t * N + row] = (uint16_t)f32_to_bf16(s);
+            if ((lane & ((1 << shift) - 1)) == 0 && idx < kGvRows * T && row < N) {
+                if constexpr (F) finish(e, t, row, s);
+                else out[(size_t)t * N + row] = (uint16_t)f32_to_bf16(s);
+            }
 #pragma unroll
             for (int q = 0; q < M; ++q) acc[q] = 0.f;
         }
@@ -260,13 +311,14 @@ __global__ __launch_bounds__(kGvThreads) void int8_gemv_kernel(const uint16_t *_
 // workgroup, so L2 hits) with the weights, converted in registers: no LDS
 // staging and no barrier before the first product.  The four wave sums
 // meet in LDS (added in wave order).
-template <int T>
+template <int T, bool F>
 __global__ __launch_bounds__(kGvThreads) void int8_gemv_rowsplit_kernel(const uint16_t *__restrict__ x,
                                                                         const int32_t *__restrict__ wq,
                                                                         const uint16_t *__restrict__ wscale,
                                                                         int N, int K, int gshift,
-                                                                        uint16_t *__restrict__ out)
+                                                                        uint16_t *__restrict__ out, Int8Epilogue e)
 {
+    const size_t xstride = F ? e.x_stride : (size_t)K;
     __shared__ float s_red[kGvThreads / 64][4];
     const int CPR = K >> 4;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -288,7 +340,7 @@ __global__ __launch_bounds__(kGvThreads) void int8_gemv_rowsplit_kernel(const ui
         r.s = srow[(16 * c) >> gshift];
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            const u32x4_t *xp = reinterpret_cast<const u32x4_t *>(x + (size_t)t * K) + 2 * c;
+            const u32x4_t *xp = reinterpret_cast<const u32x4_t *>(x + t * xstride) + 2 * c;
             r.xb[t][0] = xp[0];
             r.xb[t][1] = xp[1];
         }
@@ -341,7 +393,8 @@ __global__ __launch_bounds__(kGvThreads) void int8_gemv_rowsplit_kernel(const ui
     if (threadIdx.x < T) {
         const float v = ((s_red[0][threadIdx.x] + s_red[1][threadIdx.x]) + s_red[2][threadIdx.x]) +
                         s_red[3][threadIdx.x];
-        out[(size_t)threadIdx.x * N + row] = (uint16_t)f32_to_bf16(v);
+        if constexpr (F) finish(e, threadIdx.x, row, v);
+        else out[(size_t)threadIdx.x * N + row] = (uint16_t)f32_to_bf16(v);
     }
 }
 
@@ -364,12 +417,14 @@ constexpr int kMfRows = 16;
 
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
+template <bool F>
 __global__ __launch_bounds__(kGvThreads) void int8_gemv_mfma_kernel(const uint16_t *__restrict__ x,
                                                                    const int32_t *__restrict__ wq,
                                                                    const uint16_t *__restrict__ wscale,
                                                                    int T, int N, int K, int gshift,
-                                                                   uint16_t *__restrict__ out)
+                                                                   uint16_t *__restrict__ out, Int8Epilogue e)
 {
+    const size_t xstride = F ? e.x_stride : (size_t)K;
     // x as fp16 [T][K / 8 + 1] 16-byte units (one unit of padding per row so
     // the 16 token rows of a read fall in different banks)
     extern __shared__ u32x4_t s_x[];
@@ -418,7 +473,7 @@ __global__ __launch_bounds__(kGvThreads) void int8_gemv_mfma_kernel(const uint16
     }
     for (int i = threadIdx.x; i < T * K8; i += kGvThreads) {
         const int t = i / K8, c = i - t * K8;
-        s_x[t * xs + c] = bf16x8_to_f16x8(*reinterpret_cast<const u32x4_t *>(x + (size_t)t * K + 8 * c));
+        s_x[t * xs + c] = bf16x8_to_f16x8(*reinterpret_cast<const u32x4_t *>(x + t * xstride + 8 * c));
     }
     __syncthreads();
     if (U == 0) return;
@@ -459,7 +514,10 @@ __global__ __launch_bounds__(kGvThreads) void int8_gemv_mfma_kernel(const uint16
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int t = 4 * kq + j;
-                if (t < T && row < N) out[(size_t)t * N + row] = (uint16_t)f32_to_bf16(acc[j]);
+                if (t < T && row < N) {
+                    if constexpr (F) finish(e, t, row, acc[j]);
+                    else out[(size_t)t * N + row] = (uint16_t)f32_to_bf16(acc[j]);
+                }
                 acc[j] = 0.f;
             }
             cst = 0;
@@ -512,6 +570,7 @@ struct Int8GemmArgs {
     size_t pstride;           // T * N rounded up to a multiple of 4
     int T, N, K, gshift;
     int mtiles, ntiles, ksplit, kslice;
+    Int8Epilogue e;           // fused variant
 };
 
 // Tile: 128 tokens x 128 weight rows, K range [k0, k0 + len).  Wave w owns
@@ -520,9 +579,10 @@ struct Int8GemmArgs {
 // inputs 8 j .. 8 j + 7 and on lanes 32-63 inputs 32 + 8 j .., for both
 // operands, so each lane reads 32 contiguous bytes of its weight row per
 // stage.  GS = G / 64 stages make up one scale group.
-template <int GS>
+template <int GS, bool F>
 __global__ __launch_bounds__(kGmThreads, 2) void int8_gemm_kernel(Int8GemmArgs g)
 {
+    const size_t xstride = F ? g.e.x_stride : (size_t)g.K;
     constexpr int D = 2;   // register sets of loads in flight
     __shared__ __align__(16) _Float16 s_a[2][kGmM * kGmLds];
 
@@ -548,7 +608,7 @@ __global__ __launch_bounds__(kGmThreads, 2) void int8_gemm_kernel(Int8GemmArgs g
 #pragma unroll
     for (int o = 0; o < 4; ++o) {
         const int row = r8 + 32 * o;
-        asrc[o] = g.x + (size_t)(m0 + (row < rows ? row : 0)) * g.K + k0 + 8 * c8;
+        asrc[o] = g.x + (m0 + (row < rows ? row : 0)) * xstride + k0 + 8 * c8;
     }
     u32x4_t ra[D][4];
 
@@ -693,7 +753,8 @@ __global__ __launch_bounds__(kGmThreads, 2) void int8_gemm_kernel(Int8GemmArgs g
     // rows of the tile coalesced ----
     float *s_c = reinterpret_cast<float *>(&s_a[0][0]);
     static_assert(64 * kGmCs * sizeof(float) <= sizeof(s_a), "64 fp32 token rows fit the activation buffers");
-    const bool vec = (g.N & 3) == 0;   // every 4-column group starts 8-byte aligned (bf16) / 16-byte (fp32)
+    // every 4-column group starts 8-byte aligned (bf16) / 16-byte (fp32)
+    const bool vec = F && g.ksplit == 1 ? g.e.vec : (g.N & 3) == 0;
     float *part = g.part + (size_t)split * g.pstride;
 #pragma unroll
     for (int hp = 0; hp < 2; ++hp) {
@@ -714,7 +775,9 @@ __global__ __launch_bounds__(kGmThreads, 2) void int8_gemm_kernel(Int8GemmArgs g
             const float4 v = *reinterpret_cast<const float4 *>(s_c + r * kGmCs + c4);
             const size_t o = (size_t)(m0 + m) * g.N + nn;
             if (vec) {
-                if (g.ksplit == 1)
+                if (F && g.ksplit == 1)
+                    finish4(g.e, m0 + m, nn, v);
+                else if (g.ksplit == 1)
                     *reinterpret_cast<uint2 *>(g.out + o) =
                         make_uint2(f32x2_to_bf16x2(v.x, v.y), f32x2_to_bf16x2(v.z, v.w));
                 else
@@ -724,7 +787,8 @@ __global__ __launch_bounds__(kGmThreads, 2) void int8_gemm_kernel(Int8GemmArgs g
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if (nn + e >= g.N) break;
-                    if (g.ksplit == 1) g.out[o + e] = (uint16_t)f32_to_bf16(e4[e]);
+                    if (F && g.ksplit == 1) finish(g.e, m0 + m, nn + e, e4[e]);
+                    else if (g.ksplit == 1) g.out[o + e] = (uint16_t)f32_to_bf16(e4[e]);
                     else part[o + e] = e4[e];
                 }
             }
@@ -755,9 +819,10 @@ constexpr size_t go_lds_bytes()
     return x > c ? x : c;
 }
 
-template <int NS, int GS>
+template <int NS, int GS, bool F>
 __global__ __launch_bounds__(kGoThreads, 1) void int8_gemm_short_kernel(Int8GemmArgs g)
 {
+    const size_t xstride = F ? g.e.x_stride : (size_t)g.K;
     constexpr int LR = NS * kGmKS + 8;    // padded activation row (fp16)
     constexpr int CH = NS * 8;            // 16-byte chunks per activation row
     constexpr int XPER = (kGmM * CH + kGoThreads - 1) / kGoThreads;
@@ -792,7 +857,7 @@ __global__ __launch_bounds__(kGoThreads, 1) void int8_gemm_short_kernel(Int8Gemm
 #pragma unroll
     for (int u = 0; u < XPER; ++u) {
         const int c = min(tid + kGoThreads * u, kGmM * CH - 1), r = c / CH, col = c % CH;
-        rx[u] = *reinterpret_cast<const u32x4_t *>(g.x + (size_t)(m0 + (r < rows ? r : 0)) * g.K + 8 * col);
+        rx[u] = *reinterpret_cast<const u32x4_t *>(g.x + (m0 + (r < rows ? r : 0)) * xstride + 8 * col);
     }
     const int gpr = g.K >> g.gshift;   // groups per weight row
     uint32_t rsc[SPER];
@@ -865,7 +930,7 @@ __global__ __launch_bounds__(kGoThreads, 1) void int8_gemm_short_kernel(Int8Gemm
     // ---- epilogue through LDS, 64 tokens at a time (as in int8_gemm_kernel) ----
     __syncthreads();   // every wave is done reading the activations
     float *s_c = reinterpret_cast<float *>(s_raw);
-    const bool vec = (g.N & 3) == 0;
+    const bool vec = F ? g.e.vec : (g.N & 3) == 0;
 #pragma unroll
     for (int hp = 0; hp < 2; ++hp) {
         if (64 * hp >= rows) break;   // uniform over the workgroup
@@ -885,14 +950,18 @@ __global__ __launch_bounds__(kGoThreads, 1) void int8_gemm_short_kernel(Int8Gemm
             const float4 v = *reinterpret_cast<const float4 *>(s_c + r * kGoCs + c4);
             const size_t o = (size_t)(m0 + m) * g.N + nn;
             if (vec) {
-                *reinterpret_cast<uint2 *>(g.out + o) =
-                    make_uint2(f32x2_to_bf16x2(v.x, v.y), f32x2_to_bf16x2(v.z, v.w));
+                if constexpr (F)
+                    finish4(g.e, m0 + m, nn, v);
+                else
+                    *reinterpret_cast<uint2 *>(g.out + o) =
+                        make_uint2(f32x2_to_bf16x2(v.x, v.y), f32x2_to_bf16x2(v.z, v.w));
             } else {
                 const float e4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if (nn + e >= g.N) break;
-                    g.out[o + e] = (uint16_t)f32_to_bf16(e4[e]);
+                    if constexpr (F) finish(g.e, m0 + m, nn + e, e4[e]);
+                    else g.out[o + e] = (uint16_t)f32_to_bf16(e4[e]);
                 }
             }
         }
@@ -940,6 +1009,38 @@ __global__ __launch_bounds__(kSumThreads) void int8_splitk_sum_kernel(const floa
         for (int s = 1; s < ksplit; ++s) a += part[(size_t)s * pstride + e];
         out[e] = (uint16_t)f32_to_bf16(a);
     }
+}
+
+// The fused variant's sum over the K splits: the partials of four columns of
+// one token per thread (or of one column, where N or an operand's alignment
+// allows no more), added in split order, then the epilogue.
+__global__ __launch_bounds__(kSumThreads) void int8_splitk_epilogue_kernel(const float *__restrict__ part, int T,
+                                                                           int N, size_t pstride, int ksplit,
+                                                                           Int8Epilogue e)
+{
+    const size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x;
+    if (e.vec) {   // N is a multiple of 4
+        const int per = N >> 2;
+        const int t = (int)(i / per), r = 4 * (int)(i % per);
+        if (t >= T) return;
+        const float *p = part + (size_t)t * N + r;
+        float4 v[kInt8MaxSplitK];
+#pragma unroll
+        for (int s = 0; s < kInt8MaxSplitK; ++s)
+            if (s < ksplit) v[s] = *reinterpret_cast<const float4 *>(p + s * pstride);
+        float4 a = v[0];
+#pragma unroll
+        for (int s = 1; s < kInt8MaxSplitK; ++s)
+            if (s < ksplit) a = make_float4(a.x + v[s].x, a.y + v[s].y, a.z + v[s].z, a.w + v[s].w);
+        finish4(e, t, r, a);
+        return;
+    }
+    const int t = (int)(i / N), r = (int)(i % N);
+    if (t >= T) return;
+    const float *p = part + i;
+    float a = p[0];
+    for (int s = 1; s < ksplit; ++s) a += p[s * pstride];
+    finish(e, t, r, a);
 }
 
 }  // namespace
@@ -990,17 +1091,20 @@ Int8Plan int8_plan(int T, int N, int K, int G)
     return p;
 }
 
-hipError_t launch_int8_linear(const uint16_t *x, const int32_t *wq, const uint16_t *ws, int T, int N,
-                              int K, int G, uint16_t *out, void *workspace, hipStream_t st)
+namespace {
+
+// One launch of the plan; F: with the epilogue e (out is then unused).
+template <bool F>
+hipError_t launch_plan(const Int8Plan &p, const uint16_t *x, const int32_t *wq, const uint16_t *ws, int T, int N,
+                       int K, int G, uint16_t *out, const Int8Epilogue &e, void *workspace, hipStream_t st)
 {
-    const Int8Plan p = int8_plan(T, N, K, G);
     const int gshift = G == 64 ? 6 : 7;
     if (p.gemv && p.rowsplit) {
         switch (T) {
-        case 1: int8_gemv_rowsplit_kernel<1><<<N, kGvThreads, 0, st>>>(x, wq, ws, N, K, gshift, out); break;
-        case 2: int8_gemv_rowsplit_kernel<2><<<N, kGvThreads, 0, st>>>(x, wq, ws, N, K, gshift, out); break;
-        case 3: int8_gemv_rowsplit_kernel<3><<<N, kGvThreads, 0, st>>>(x, wq, ws, N, K, gshift, out); break;
-        default: int8_gemv_rowsplit_kernel<4><<<N, kGvThreads, 0, st>>>(x, wq, ws, N, K, gshift, out); break;
+        case 1: int8_gemv_rowsplit_kernel<1, F><<<N, kGvThreads, 0, st>>>(x, wq, ws, N, K, gshift, out, e); break;
+        case 2: int8_gemv_rowsplit_kernel<2, F><<<N, kGvThreads, 0, st>>>(x, wq, ws, N, K, gshift, out, e); break;
+        case 3: int8_gemv_rowsplit_kernel<3, F><<<N, kGvThreads, 0, st>>>(x, wq, ws, N, K, gshift, out, e); break;
+        default: int8_gemv_rowsplit_kernel<4, F><<<N, kGvThreads, 0, st>>>(x, wq, ws, N, K, gshift, out, e); break;
         }
         return hipGetLastError();
     }
@@ -1010,7 +1114,7 @@ hipError_t launch_int8_linear(const uint16_t *x, const int32_t *wq, const uint16
         int grid = (nrb + wpb - 1) / wpb;
         grid = grid < kInt8GemvMaxBlocks ? grid : kInt8GemvMaxBlocks;
         const size_t lds = (size_t)T * (K / 8 + 1) * 16;
-        int8_gemv_mfma_kernel<<<grid, kGvThreads, lds, st>>>(x, wq, ws, T, N, K, gshift, out);
+        int8_gemv_mfma_kernel<F><<<grid, kGvThreads, lds, st>>>(x, wq, ws, T, N, K, gshift, out, e);
         return hipGetLastError();
     }
     if (p.gemv) {
@@ -1020,10 +1124,10 @@ hipError_t launch_int8_linear(const uint16_t *x, const int32_t *wq, const uint16
         grid = grid < kInt8GemvMaxBlocks ? grid : kInt8GemvMaxBlocks;
         const size_t lds = (size_t)T * K * 2 + (size_t)T * (K / 16) * 4;
         switch (T) {
-        case 1: int8_gemv_kernel<1><<<grid, kGvThreads, lds, st>>>(x, wq, ws, N, K, gshift, out); break;
-        case 2: int8_gemv_kernel<2><<<grid, kGvThreads, lds, st>>>(x, wq, ws, N, K, gshift, out); break;
-        case 3: int8_gemv_kernel<3><<<grid, kGvThreads, lds, st>>>(x, wq, ws, N, K, gshift, out); break;
-        default: int8_gemv_kernel<4><<<grid, kGvThreads, lds, st>>>(x, wq, ws, N, K, gshift, out); break;
+        case 1: int8_gemv_kernel<1, F><<<grid, kGvThreads, lds, st>>>(x, wq, ws, N, K, gshift, out, e); break;
+        case 2: int8_gemv_kernel<2, F><<<grid, kGvThreads, lds, st>>>(x, wq, ws, N, K, gshift, out, e); break;
+        case 3: int8_gemv_kernel<3, F><<<grid, kGvThreads, lds, st>>>(x, wq, ws, N, K, gshift, out, e); break;
+        default: int8_gemv_kernel<4, F><<<grid, kGvThreads, lds, st>>>(x, wq, ws, N, K, gshift, out, e); break;
         }
         return hipGetLastError();
     }
@@ -1042,33 +1146,56 @@ hipError_t launch_int8_linear(const uint16_t *x, const int32_t *wq, const uint16
     a.ksplit = p.ksplit;
     a.kslice = p.kslice;
     a.pstride = p.pstride;
+    a.e = e;
     const long tiles = (long)p.mtiles * p.ntiles * p.ksplit;
     const int grid = (int)((tiles + 7) / 8 * 8);
     if (p.short_k) {
         const int ns = K / kGmKS;
         if (G == 64) {
             switch (ns) {
-            case 1: int8_gemm_short_kernel<1, 1><<<grid, kGoThreads, 0, st>>>(a); break;
-            case 2: int8_gemm_short_kernel<2, 1><<<grid, kGoThreads, 0, st>>>(a); break;
-            case 3: int8_gemm_short_kernel<3, 1><<<grid, kGoThreads, 0, st>>>(a); break;
-            case 4: int8_gemm_short_kernel<4, 1><<<grid, kGoThreads, 0, st>>>(a); break;
-            default: int8_gemm_short_kernel<5, 1><<<grid, kGoThreads, 0, st>>>(a); break;
+            case 1: int8_gemm_short_kernel<1, 1, F><<<grid, kGoThreads, 0, st>>>(a); break;
+            case 2: int8_gemm_short_kernel<2, 1, F><<<grid, kGoThreads, 0, st>>>(a); break;
+            case 3: int8_gemm_short_kernel<3, 1, F><<<grid, kGoThreads, 0, st>>>(a); break;
+            case 4: int8_gemm_short_kernel<4, 1, F><<<grid, kGoThreads, 0, st>>>(a); break;
+            default: int8_gemm_short_kernel<5, 1, F><<<grid, kGoThreads, 0, st>>>(a); break;
             }
         } else {
-            if (ns == 2) int8_gemm_short_kernel<2, 2><<<grid, kGoThreads, 0, st>>>(a);
-            else int8_gemm_short_kernel<4, 2><<<grid, kGoThreads, 0, st>>>(a);
+            if (ns == 2) int8_gemm_short_kernel<2, 2, F><<<grid, kGoThreads, 0, st>>>(a);
+            else int8_gemm_short_kernel<4, 2, F><<<grid, kGoThreads, 0, st>>>(a);
         }
         return hipGetLastError();
     }
-    if (G == 64) int8_gemm_kernel<1><<<grid, kGmThreads, 0, st>>>(a);
-    else int8_gemm_kernel<2><<<grid, kGmThreads, 0, st>>>(a);
+    if (G == 64) int8_gemm_kernel<1, F><<<grid, kGmThreads, 0, st>>>(a);
+    else int8_gemm_kernel<2, F><<<grid, kGmThreads, 0, st>>>(a);
     if (p.ksplit > 1) {
         const size_t count = (size_t)T * N;
+        if (F) {
+            const size_t threads = e.vec ? count / 4 : count;
+            int8_splitk_epilogue_kernel<<<(unsigned)((threads + kSumThreads - 1) / kSumThreads), kSumThreads, 0,
+                                          st>>>(a.part, T, N, p.pstride, p.ksplit, e);
+            return hipGetLastError();
+        }
         const size_t threads = (count + 3) / 4;
         int8_splitk_sum_kernel<<<(unsigned)((threads + kSumThreads - 1) / kSumThreads), kSumThreads, 0, st>>>(
             a.part, count, p.pstride, p.ksplit, out);
     }
     return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_int8_linear(const uint16_t *x, const int32_t *wq, const uint16_t *ws, int T, int N,
+                              int K, int G, uint16_t *out, void *workspace, hipStream_t st)
+{
+    return launch_plan<false>(int8_plan(T, N, K, G), x, wq, ws, T, N, K, G, out, Int8Epilogue{}, workspace, st);
+}
+
+Int8Plan int8_fused_plan(int T, int N, int K, int G) { return int8_plan(T, N, K, G); }
+
+hipError_t launch_int8_linear_fused(const uint16_t *x, const int32_t *wq, const uint16_t *ws, int T, int N,
+                                    int K, int G, const Int8Epilogue &e, void *workspace, hipStream_t st)
+{
+    return launch_plan<true>(int8_fused_plan(T, N, K, G), x, wq, ws, T, N, K, G, nullptr, e, workspace, st);
 }
 
 }  // namespace moe
