@@ -328,12 +328,13 @@ int32_t moe_int8_linear_fused(const uint16_t *x, int64_t x_stride, const int32_t
  *   bias_ids int32, bias_values fp32 [rows][bias_width], rows bias_stride
  *            elements apart; bias_lengths int32 [rows] (NULL: every entry),
  *            clamped to [0, bias_width].  Of a token listed twice the last
- *            entry holds.
+ *            entry holds; a subnormal value counts as zero.
  *   temperature  fp32 [rows] (NULL: 1); a row whose temperature is not above
  *            zero (greedy) is not scaled
  *   mask     uint32 words, rows mask_stride words apart (0: one row for all):
  *            bit v % 32 of word v / 32 is set where token v is allowed
- * Ids outside [0, vocab) (padding) are ignored. */
+ * Ids outside [0, vocab) (padding) are ignored.  The tables are read beyond
+ * the lengths too, up to their widths. */
 typedef struct moe_int4_logits_rules {
     const int32_t *history;
     const int32_t *history_lengths;

@@ -253,21 +253,32 @@ def type_code(dtype) -> int:
 def row_stride(t, name: str, rows: int, cols: int) -> int:
     """The row stride of a matrix argument of `rows` x `cols`, its elements
     consecutive in a row."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} is {tuple(t.shape)}, expected ({rows}, {cols})")
-    if cols > 1 and t.stride(1) != 1:
+    stride = t.stride()
+    if stride[1] != 1 and cols > 1:
         raise ValueError(f"{name}: the elements of a row must be consecutive")
-    return t.stride(0)
+    return stride[0]
 
 
-def on_device(device, **tensors):
-    """Every tensor given lies on `device`, a GPU: the library dereferences
-    its address there."""
-    if device.type != "cuda":
-        raise ValueError(f"the tensors must be on the GPU, not on {device}")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+def device_index(t, name: str, index: int | None = None) -> int:
+    """The index of the GPU that holds t (`index`, where one is expected): the
+    library dereferences t's address there."""
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"{name} must be on the GPU, it is on {t.device}")
+    if index is not None and i != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    return i
+
+
+def _stream_on(stream, index: int) -> int | None:
+    """The given stream, or torch's current one on a device (its handle alone:
+    building the stream object costs as much as a launch's other checks)."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
 def moe_int8_linear_fused_workspace_bytes(tokens: int, n: int, k: int, group: int) -> int:
@@ -283,25 +294,32 @@ def moe_int8_linear_fused(x, w_packed, w_scales, tokens: int, n: int, k: int, gr
     [tokens, n]; bias, residual and out in bf16, fp16 or fp32, the rows of x,
     residual and out possibly inside wider ones.  activation: a key of
     ACTIVATIONS.  workspace: uint8, may be None when the shape needs none."""
-    if activation not in ACTIVATIONS:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation {activation!r} is none of {', '.join(ACTIVATIONS)}")
     if type_code(x.dtype) != TYPE_BF16:
         raise ValueError(f"x is {x.dtype}, expected bfloat16 (or its bits)")
-    xs, os_ = row_stride(x, "x", tokens, k), row_stride(out, "out", tokens, n)
+    x_stride, out_stride = row_stride(x, "x", tokens, k), row_stride(out, "out", tokens, n)
     out_type = type_code(out.dtype)
-    e = MoeInt8Epilogue(activation=ACTIVATIONS[activation])
+    e = MoeInt8Epilogue(None, None, 0, 0, 0, act)
     if bias is not None:
-        if bias.dim() != 1 or bias.shape[0] != n or (n > 1 and bias.stride(0) != 1):
+        if bias.shape != (n,) or not bias.is_contiguous():
             raise ValueError(f"bias is {tuple(bias.shape)}, expected ({n},), contiguous")
         e.bias, e.bias_type = bias.data_ptr(), type_code(bias.dtype)
     if residual is not None:
         e.residual_stride = row_stride(residual, "residual", tokens, n)
         e.residual, e.residual_type = residual.data_ptr(), type_code(residual.dtype)
-    on_device(x.device, w_packed=w_packed, w_scales=w_scales, out=out, bias=bias, residual=residual,
-              workspace=workspace)
-    _check(lib().moe_int8_linear_fused(x.data_ptr(), xs, w_packed.data_ptr(), w_scales.data_ptr(), tokens, n, k,
-                                       group, ctypes.byref(e), out.data_ptr(), out_type, os_, _ptr(workspace),
-                                       0 if workspace is None else workspace.numel(), _stream(stream)))
+    index = device_index(x, "x")
+    for name, t in (("w_packed", w_packed), ("w_scales", w_scales), ("out", out), ("bias", bias),
+                    ("residual", residual), ("workspace", workspace)):
+        if t is not None:
+            device_index(t, name, index)
+    rc = lib().moe_int8_linear_fused(x.data_ptr(), x_stride, w_packed.data_ptr(), w_scales.data_ptr(), tokens, n, k,
+                                     group, ctypes.byref(e), out.data_ptr(), out_type, out_stride,
+                                     _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                     _stream_on(stream, index))
+    if rc:
+        _check(rc)
 
 
 def moe_int4_logits_process(logits, rules: MoeLogitsRules, out, stream=None):
@@ -312,11 +330,14 @@ def moe_int4_logits_process(logits, rules: MoeLogitsRules, out, stream=None):
     if logits.dim() != 2:
         raise ValueError(f"logits is {tuple(logits.shape)}, expected [rows, vocab]")
     rows, vocab = logits.shape
-    ls, os_ = row_stride(logits, "logits", rows, vocab), row_stride(out, "out", rows, vocab)
-    on_device(logits.device, out=out)
-    _check(lib().moe_int4_logits_process(logits.data_ptr(), type_code(logits.dtype), ls, rows, vocab,
-                                         ctypes.byref(rules), out.data_ptr(), type_code(out.dtype), os_,
-                                         _stream(stream)))
+    stride, out_stride = row_stride(logits, "logits", rows, vocab), row_stride(out, "out", rows, vocab)
+    in_type, out_type = type_code(logits.dtype), type_code(out.dtype)
+    index = device_index(logits, "logits")
+    device_index(out, "out", index)
+    rc = lib().moe_int4_logits_process(logits.data_ptr(), in_type, stride, rows, vocab, ctypes.byref(rules),
+                                       out.data_ptr(), out_type, out_stride, _stream_on(stream, index))
+    if rc:
+        _check(rc)
 
 
 def version() -> str:

@@ -95,19 +95,19 @@ class Int8Linear:
                 out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
         """residual + act(x W^T + bias) on torch's current stream of x's
         device; x bf16 [tokens, k].  out may be the residual."""
-        device = x.device
-        if device.type == "cuda" and device.index != torch.cuda.current_device():
-            with torch.cuda.device(device):
+        index = x.get_device()
+        if index >= 0 and index != torch.cuda.current_device():
+            with torch.cuda.device(index):
                 return self.forward(x, residual, out, out_dtype)
         tokens = x.shape[0]
         if out is None:
-            out = torch.empty(tokens, self.n, dtype=out_dtype, device=device)
+            out = torch.empty(tokens, self.n, dtype=out_dtype, device=x.device)
         need = self._need.get(tokens)
         if need is None:
             need = self._need[tokens] = B.moe_int8_linear_fused_workspace_bytes(tokens, self.n, self.k, self.group)
         # taken anew for every call: the allocator orders it by stream, and
         # two calls in flight never share one
-        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
         B.moe_int8_linear_fused(x, self.packed, self.scales, tokens, self.n, self.k, self.group, out, self.bias,
                                 residual, self.activation, workspace)
         return out
@@ -174,9 +174,9 @@ class LogitsRules:
                 raise ValueError(f"mask has {mask.shape[1]} words a row, {self.vocab} tokens need {words}")
             c.mask_stride = 0 if shared_mask else mask.stride(0)
         self._tables = {**given, **({} if mask is None else {"mask": mask})}
-        for t in self._tables.values():
-            B.on_device(t.device, **self._tables)
-        self.device = next((t.device for t in self._tables.values()), None)
+        self._index = None   # of the GPU that holds the tables
+        for name, t in self._tables.items():
+            self._index = B.device_index(t, name, self._index)
         self._c = c
 
     def apply(self, logits: torch.Tensor, out: torch.Tensor | None = None,
@@ -184,16 +184,14 @@ class LogitsRules:
         """The rules applied to logits [rows, vocab] on torch's current stream
         of their device; the first rows of the tables where there are fewer
         logits than table rows.  out may be logits (in place)."""
-        device = logits.device
         if logits.dim() != 2 or logits.shape[1] != self.vocab or (self.rows is not None
                                                                   and logits.shape[0] > self.rows):
             raise ValueError(f"logits is {tuple(logits.shape)}, expected at most {self.rows} rows of {self.vocab}")
-        if self.device is not None and device != self.device:
-            raise ValueError(f"logits is on {device}, the rules on {self.device}")
-        if device.type == "cuda" and device.index != torch.cuda.current_device():
-            with torch.cuda.device(device):
+        index = B.device_index(logits, "logits", self._index)
+        if index != torch.cuda.current_device():
+            with torch.cuda.device(index):
                 return self.apply(logits, out, out_dtype)
         if out is None:
-            out = torch.empty(logits.shape, dtype=out_dtype, device=device)
+            out = torch.empty(logits.shape, dtype=out_dtype, device=logits.device)
         B.moe_int4_logits_process(logits, self._c, out)
         return out

@@ -329,7 +329,7 @@ def test_rules_refusals():
     logits, u = make(4, 1000, 20, 6, True, 1)
     with pytest.raises(ValueError, match="at most 4 rows"):
         LogitsRules(1000, **u).apply(torch.zeros(5, 1000, device="cuda"))
-    with pytest.raises(ValueError, match="logits is on cpu"):
+    with pytest.raises(ValueError, match="logits must be on the GPU"):
         LogitsRules(1000, **u).apply(logits.cpu())
     with pytest.raises(ValueError, match="GPU"):
         LogitsRules(1000).apply(logits.cpu())
