@@ -381,7 +381,7 @@ def test_fused_refuses_host_tensors_and_bad_shapes():
         Int8Linear(d["packed"].cpu(), d["scales"].cpu(), 64).forward(d["x"].cpu())
     with pytest.raises(ValueError, match="x is"):
         lin.forward(d["x"][:, :32])
-    with pytest.raises(ValueError, match="residual is on"):
+    with pytest.raises(ValueError, match="residual must be on the GPU"):
         lin.forward(d["x"], residual=torch.zeros(3, 16))
     with pytest.raises(ValueError, match="consecutive"):
         lin.forward(d["x"], out=torch.empty(16, 3, device="cuda").t())

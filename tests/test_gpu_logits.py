@@ -333,7 +333,7 @@ def test_rules_refusals():
         LogitsRules(1000, **u).apply(logits.cpu())
     with pytest.raises(ValueError, match="GPU"):
         LogitsRules(1000).apply(logits.cpu())
-    with pytest.raises(ValueError, match="presence is on"):
+    with pytest.raises(ValueError, match="presence must be on the GPU"):
         LogitsRules(1000, **{**u, "presence": u["presence"].cpu()})
     with pytest.raises(B.MoeError, match="out overlaps logits"):
         wide = torch.zeros(4, 1500, device="cuda")
