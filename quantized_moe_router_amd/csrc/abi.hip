@@ -593,16 +593,16 @@ struct Rows {
 };
 
 // Pointer, type, alignment and stride of one operand (one row: the stride is
-// not read).  Rows of up to 2^31 elements, 2^40 apart, keep every byte
-// offset far inside 63 bits.
+// not read).  Rows at most 2^24 elements apart: 32 of them span less than
+// 2^31 bytes, which the fused kernels' buffer offsets need.
 static int32_t check_rows(const Rows &m)
 {
     if (!m.p) return fail(MOE_INT4_EINVAL, "%s is NULL", m.name);
     if (!known_type(m.type)) return fail(MOE_INT4_EINVAL, "%s: type %d is none of MOE_TYPE_*", m.name, m.type);
     if ((uintptr_t)m.p % (uintptr_t)type_bytes(m.type))
         return fail(MOE_INT4_EALIGN, "%s is not aligned to its elements", m.name);
-    if (m.rows > 1 && (m.stride < m.cols || m.stride > ((int64_t)1 << 40)))
-        return fail(MOE_INT4_EINVAL, "%s: stride %lld outside [%lld, 2^40]", m.name, (long long)m.stride,
+    if (m.rows > 1 && (m.stride < m.cols || m.stride > ((int64_t)1 << 24)))
+        return fail(MOE_INT4_EINVAL, "%s: stride %lld outside [%lld, 2^24]", m.name, (long long)m.stride,
                     (long long)m.cols);
     return MOE_INT4_OK;
 }
@@ -631,10 +631,10 @@ static bool same_rows(const Rows &a, const Rows &b)
     return a.p == b.p && a.type == b.type && (a.rows <= 1 || a.stride == b.stride);
 }
 
-// Whether four elements at a multiple of four of every row are aligned.
-static bool rows_aligned4(const Rows &m)
+// Whether `per` elements at a multiple of `per` of every row are aligned.
+static bool rows_aligned(const Rows &m, int per)
 {
-    return (uintptr_t)m.p % (4u * type_bytes(m.type)) == 0 && (m.rows <= 1 || m.stride % 4 == 0);
+    return (uintptr_t)m.p % (unsigned)(per * type_bytes(m.type)) == 0 && (m.rows <= 1 || m.stride % per == 0);
 }
 
 static int32_t check_stream(hipStream_t st)
@@ -683,17 +683,17 @@ int32_t moe_int8_linear_fused(const uint16_t *x, int64_t x_stride, const int32_t
     if (tokens > 1 && x_stride % 8)
         return fail(MOE_INT4_EALIGN, "x: stride %lld is not a multiple of 8", (long long)x_stride);
     if (may_overlap(rx, ro)) return fail(MOE_INT4_EINVAL, "out overlaps x");
-    bool vec = n % 4 == 0 && rows_aligned4(ro);
+    bool vec = n % 4 == 0 && rows_aligned(ro, 4);
     if (e.bias) {
         if ((rc = check_rows(rb))) return rc;
         if (may_overlap(rb, ro)) return fail(MOE_INT4_EINVAL, "out overlaps bias");
-        vec = vec && rows_aligned4(rb);
+        vec = vec && rows_aligned(rb, 4);
     }
     if (e.residual) {
         if ((rc = check_rows(rr))) return rc;
         if (!same_rows(rr, ro) && may_overlap(rr, ro))
             return fail(MOE_INT4_EINVAL, "out overlaps residual without being the same rows");
-        vec = vec && rows_aligned4(rr);
+        vec = vec && rows_aligned(rr, 4);
     }
     const size_t need = int8_fused_plan(tokens, n, k, group).part_bytes;
     if (need) {

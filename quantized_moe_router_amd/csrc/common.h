@@ -524,6 +524,7 @@ struct Int8Plan {
     int mtiles, ntiles, ksplit, kslice;
     size_t pstride;      // floats per split in the partials (T * N rounded up to 4)
     size_t part_bytes;   // fp32 split-K partials (workspace)
+    bool kwaves;         // fused variant: K over the waves of a workgroup
 };
 Int8Plan int8_plan(int T, int N, int K, int G);
 hipError_t launch_int8_linear(const uint16_t *x, const int32_t *wq, const uint16_t *ws, int T, int N,
@@ -543,6 +544,10 @@ struct Int8Epilogue {
     bool vec;               // every four columns at a multiple of four are aligned in bias, residual and out
 };
 Int8Plan int8_fused_plan(int T, int N, int K, int G);
+hipError_t launch_int8_short_fused(const uint16_t *x, const int32_t *wq, const uint16_t *ws, int T, int N, int K,
+                                  int G, const Int8Epilogue &e, hipStream_t st);
+hipError_t launch_int8_ksplit(const uint16_t *x, const int32_t *wq, const uint16_t *ws, int T, int N, int K, int G,
+                              const Int8Epilogue &e, int ksplit, float *part, size_t pstride, hipStream_t st);
 hipError_t launch_int8_linear_fused(const uint16_t *x, const int32_t *wq, const uint16_t *ws, int T, int N,
                                     int K, int G, const Int8Epilogue &e, void *workspace, hipStream_t st);
 

@@ -1,0 +1,115 @@
+// Device helpers shared by the INT8 W8A16 linear layer's kernels.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+// Stored bytes 2i and 2i+1 of a word -> fp16 pair (q - 128), exact.  The
+// permute takes result bytes from {0x64646464 (bytes 4-7), w (bytes 0-3)}.
+template <int I>
+__device__ __forceinline__ h2_t code_pair(uint32_t w)
+{
+    constexpr uint32_t sel = I == 0 ? 0x04010400u : 0x04030402u;
+    const uint32_t p = __builtin_amdgcn_perm(0x64646464u, w, sel);
+    return __builtin_bit_cast(h2_t, p) + h2_t{(_Float16)-1152.f, (_Float16)-1152.f};
+}
+
+// 8 bf16 (natural order) -> 8 fp16 (natural order); exact in fp16's normal
+// range, toward zero outside it (saturating at 65504).
+__device__ __forceinline__ u32x4_t bf16x8_to_f16x8(u32x4_t v)
+{
+    u32x4_t o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        o[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(bf16_lo(v[j]), bf16_hi(v[j])));
+    return o;
+}
+
+// ---------------------------------------------------------------------------
+// Epilogue of the fused variant (F = true in the kernels below):
+//   out[t][r] = rnd(residual[t][r] + act(sum + bias[r]))
+// in fp32, one rounding.  Everything happens on the sum in registers, so the
+// activation and the addition cost no pass over [T][N] of their own.
+// exp, erfc and the division are the accurate ones: an fp32 output shows
+// errors that a bf16 one would hide.
+// ---------------------------------------------------------------------------
+template <int KIND>
+__device__ __forceinline__ float activate_as(float v)
+{
+    if constexpr (KIND == kActRelu) return v < 0.f ? 0.f : v;   // a NaN passes
+    if constexpr (KIND == kActSilu) return v / (1.f + expf(-v));
+    if constexpr (KIND == kActGelu) return 0.5f * v * erfcf(-0.70710678118654752f * v);
+    if constexpr (KIND == kActGeluTanh) {
+        // 0.5 (1 + tanh u) = 1 / (1 + e^-2u), without tanh's cancellation near -1
+        const float u = 0.79788456080286536f * fmaf(0.044715f * v * v, v, v);
+        return v / (1.f + expf(-2.f * u));
+    }
+    if constexpr (KIND == kActSigmoid) return 1.f / (1.f + expf(-v));
+    return v;
+}
+
+// M values at a time; the kind is uniform over the launch.
+template <int M>
+__device__ __forceinline__ void activate(float (&v)[M], int kind)
+{
+    switch (kind) {
+    case kActRelu:
+#pragma unroll
+        for (int i = 0; i < M; ++i) v[i] = activate_as<kActRelu>(v[i]);
+        break;
+    case kActSilu:
+#pragma unroll
+        for (int i = 0; i < M; ++i) v[i] = activate_as<kActSilu>(v[i]);
+        break;
+    case kActGelu:
+#pragma unroll
+        for (int i = 0; i < M; ++i) v[i] = activate_as<kActGelu>(v[i]);
+        break;
+    case kActGeluTanh:
+#pragma unroll
+        for (int i = 0; i < M; ++i) v[i] = activate_as<kActGeluTanh>(v[i]);
+        break;
+    case kActSigmoid:
+#pragma unroll
+        for (int i = 0; i < M; ++i) v[i] = activate_as<kActSigmoid>(v[i]);
+        break;
+    default: break;
+    }
+}
+__device__ __forceinline__ float activate(float v, int kind)
+{
+    float a[1] = {v};
+    activate(a, kind);
+    return a[0];
+}
+
+__device__ __forceinline__ void finish(const Int8Epilogue &e, int t, int r, float v)
+{
+    if (e.bias) v += load_typed(e.bias, e.bias_type, r);
+    v = activate(v, e.activation);
+    if (e.residual) v += load_typed(e.residual, e.residual_type, t * e.residual_stride + r);
+    store_typed(e.out, e.out_type, t * e.out_stride + r, v);
+}
+
+// Columns r .. r + 3 of one row (r a multiple of 4, e.vec set).
+__device__ __forceinline__ void finish4(const Int8Epilogue &e, int t, int r, float4 v)
+{
+    if (e.bias) {
+        const float4 b = load_typed4(e.bias, e.bias_type, r);
+        v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+    }
+    v = make_float4(activate(v.x, e.activation), activate(v.y, e.activation), activate(v.z, e.activation),
+                    activate(v.w, e.activation));
+    if (e.residual) {
+        const float4 b = load_typed4(e.residual, e.residual_type, t * e.residual_stride + r);
+        v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+    }
+    store_typed4(e.out, e.out_type, t * e.out_stride + r, v);
+}
+
+}  // namespace moe

@@ -38,25 +38,11 @@
 //     fp32 partials summed in a fixed order (deterministic).
 #include <type_traits>
 
-#include "common.h"
+#include "int8.h"
 
 namespace moe {
 
 namespace {
-
-typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
-
-// Stored bytes 2i and 2i+1 of a word -> fp16 pair (q - 128), exact.  The
-// permute takes result bytes from {0x64646464 (bytes 4-7), w (bytes 0-3)}.
-template <int I>
-__device__ __forceinline__ h2_t code_pair(uint32_t w)
-{
-    constexpr uint32_t sel = I == 0 ? 0x04010400u : 0x04030402u;
-    const uint32_t p = __builtin_amdgcn_perm(0x64646464u, w, sel);
-    return __builtin_bit_cast(h2_t, p) + h2_t{(_Float16)-1152.f, (_Float16)-1152.f};
-}
 
 // Stored bytes 2i and 2i+1 -> fp16 pair (1024 + q), exact; the caller
 // removes the bias (1152 per unit of the activation sum) once per chunk.
@@ -65,65 +51,6 @@ __device__ __forceinline__ h2_t code_pair_biased(uint32_t w)
 {
     constexpr uint32_t sel = I == 0 ? 0x04010400u : 0x04030402u;
     return __builtin_bit_cast(h2_t, __builtin_amdgcn_perm(0x64646464u, w, sel));
-}
-
-// 8 bf16 (natural order) -> 8 fp16 (natural order); exact in fp16's normal
-// range, toward zero outside it (saturating at 65504).
-__device__ __forceinline__ u32x4_t bf16x8_to_f16x8(u32x4_t v)
-{
-    u32x4_t o;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        o[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(bf16_lo(v[j]), bf16_hi(v[j])));
-    return o;
-}
-
-// ---------------------------------------------------------------------------
-// Epilogue of the fused variant (F = true in the kernels below):
-//   out[t][r] = rnd(residual[t][r] + act(sum + bias[r]))
-// in fp32, one rounding.  Everything happens on the sum in registers, so the
-// activation and the addition cost no pass over [T][N] of their own.
-// exp, erfc and the division are the accurate ones: an fp32 output shows
-// errors that a bf16 one would hide.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ float activate(float v, int kind)
-{
-    switch (kind) {   // uniform over the launch
-    case kActRelu: return v < 0.f ? 0.f : v;   // a NaN passes
-    case kActSilu: return v / (1.f + expf(-v));
-    case kActGelu: return 0.5f * v * erfcf(-0.70710678118654752f * v);
-    case kActGeluTanh: {
-        // 0.5 (1 + tanh u) = 1 / (1 + e^-2u), without tanh's cancellation near -1
-        const float u = 0.79788456080286536f * fmaf(0.044715f * v * v, v, v);
-        return v / (1.f + expf(-2.f * u));
-    }
-    case kActSigmoid: return 1.f / (1.f + expf(-v));
-    default: return v;
-    }
-}
-
-__device__ __forceinline__ void finish(const Int8Epilogue &e, int t, int r, float v)
-{
-    if (e.bias) v += load_typed(e.bias, e.bias_type, r);
-    v = activate(v, e.activation);
-    if (e.residual) v += load_typed(e.residual, e.residual_type, t * e.residual_stride + r);
-    store_typed(e.out, e.out_type, t * e.out_stride + r, v);
-}
-
-// Columns r .. r + 3 of one row (r a multiple of 4, e.vec set).
-__device__ __forceinline__ void finish4(const Int8Epilogue &e, int t, int r, float4 v)
-{
-    if (e.bias) {
-        const float4 b = load_typed4(e.bias, e.bias_type, r);
-        v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
-    }
-    v = make_float4(activate(v.x, e.activation), activate(v.y, e.activation), activate(v.z, e.activation),
-                    activate(v.w, e.activation));
-    if (e.residual) {
-        const float4 b = load_typed4(e.residual, e.residual_type, t * e.residual_stride + r);
-        v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
-    }
-    store_typed4(e.out, e.out_type, t * e.out_stride + r, v);
 }
 
 __device__ __forceinline__ float xor_shfl(float v, int m) { return __shfl_xor(v, m, 64); }
@@ -1093,6 +1020,15 @@ Int8Plan int8_plan(int T, int N, int K, int G)
 
 namespace {
 
+hipError_t launch_splitk_epilogue(const Int8Plan &p, int T, int N, const Int8Epilogue &e, const float *part,
+                                  hipStream_t st)
+{
+    const size_t count = (size_t)T * N, threads = e.vec ? count / 4 : count;
+    int8_splitk_epilogue_kernel<<<(unsigned)((threads + kSumThreads - 1) / kSumThreads), kSumThreads, 0, st>>>(
+        part, T, N, p.pstride, p.ksplit, e);
+    return hipGetLastError();
+}
+
 // One launch of the plan; F: with the epilogue e (out is then unused).
 template <bool F>
 hipError_t launch_plan(const Int8Plan &p, const uint16_t *x, const int32_t *wq, const uint16_t *ws, int T, int N,
@@ -1169,12 +1105,7 @@ hipError_t launch_plan(const Int8Plan &p, const uint16_t *x, const int32_t *wq, 
     else int8_gemm_kernel<2, F><<<grid, kGmThreads, 0, st>>>(a);
     if (p.ksplit > 1) {
         const size_t count = (size_t)T * N;
-        if (F) {
-            const size_t threads = e.vec ? count / 4 : count;
-            int8_splitk_epilogue_kernel<<<(unsigned)((threads + kSumThreads - 1) / kSumThreads), kSumThreads, 0,
-                                          st>>>(a.part, T, N, p.pstride, p.ksplit, e);
-            return hipGetLastError();
-        }
+        if (F) return launch_splitk_epilogue(p, T, N, e, a.part, st);
         const size_t threads = (count + 3) / 4;
         int8_splitk_sum_kernel<<<(unsigned)((threads + kSumThreads - 1) / kSumThreads), kSumThreads, 0, st>>>(
             a.part, count, p.pstride, p.ksplit, out);
@@ -1190,12 +1121,40 @@ hipError_t launch_int8_linear(const uint16_t *x, const int32_t *wq, const uint16
     return launch_plan<false>(int8_plan(T, N, K, G), x, wq, ws, T, N, K, G, out, Int8Epilogue{}, workspace, st);
 }
 
-Int8Plan int8_fused_plan(int T, int N, int K, int G) { return int8_plan(T, N, K, G); }
+// The fused layer's plan: the plain one's, but for few output tiles of 32 x 32
+// K goes over the waves of a workgroup (measured with int8_gemm_kernel's time
+// behind: N = 320, K = 10240: 32 tokens 8.1 us, 10.9; 512 tokens, 160 tiles,
+// 19.4, 21.8; 1024 tokens, 320 tiles, 36.0, 29.6; N = 1003, K = 1152: 77
+// tokens 6.3, 12.4; 512 tokens, 512 tiles, 12.7, 19.5).  A K of many stages
+// per wave is split over workgroups too where the tiles leave most CUs idle:
+// 32 tokens of N = 320, K = 10240 take 17.9 us unsplit, 8.1 in 16 parts; from
+// K = 5120 that pays for the second launch.
+Int8Plan int8_fused_plan(int T, int N, int K, int G)
+{
+    Int8Plan p = int8_plan(T, N, K, G);
+    if (p.gemv || T == 0 || p.short_k) return p;
+    const long tiles = (long)((T + 31) / 32) * ((N + 31) / 32);
+    if (tiles > (K <= 2560 ? 512 : 256)) return p;
+    p.kwaves = true;
+    int ks = K >= 5120 ? (int)(192 / tiles) : 1;
+    ks = ks < kInt8MaxSplitK ? ks : kInt8MaxSplitK;
+    ks = ks < K / 1024 ? ks : K / 1024;   // a stage of 64 for each of 16 waves
+    p.ksplit = ks > 1 ? ks : 1;
+    p.part_bytes = p.ksplit > 1 ? (size_t)p.ksplit * p.pstride * 4 : 0;
+    return p;
+}
 
 hipError_t launch_int8_linear_fused(const uint16_t *x, const int32_t *wq, const uint16_t *ws, int T, int N,
                                     int K, int G, const Int8Epilogue &e, void *workspace, hipStream_t st)
 {
-    return launch_plan<true>(int8_fused_plan(T, N, K, G), x, wq, ws, T, N, K, G, nullptr, e, workspace, st);
+    const Int8Plan p = int8_fused_plan(T, N, K, G);
+    if (p.short_k && e.vec) return launch_int8_short_fused(x, wq, ws, T, N, K, G, e, st);
+    if (p.kwaves) {
+        float *part = static_cast<float *>(workspace);
+        const hipError_t rc = launch_int8_ksplit(x, wq, ws, T, N, K, G, e, p.ksplit, part, p.pstride, st);
+        return rc == hipSuccess && p.ksplit > 1 ? launch_splitk_epilogue(p, T, N, e, part, st) : rc;
+    }
+    return launch_plan<true>(p, x, wq, ws, T, N, K, G, nullptr, e, workspace, st);
 }
 
 }  // namespace moe
