@@ -516,6 +516,13 @@ constexpr long kInt8GemmTargetTiles = 256;     // K is split until about this ma
 constexpr int kInt8MinSplitK = 256;            // shortest K range of one split
 constexpr int kInt8MaxSplitK = 16;
 
+// The fused variant's GEMV with whole-line loads: K in steps, at least as many
+// as its loads run ahead; its activations fit LDS beside 22 KB of staging.
+constexpr int kInt8WideStep = 128;
+constexpr int kInt8WideAhead = 4;
+constexpr int kInt8WideMinK = kInt8WideStep * kInt8WideAhead;
+constexpr size_t kInt8WideMaxLds = 136 * 1024;
+
 struct Int8Plan {
     bool gemv;
     bool rowsplit;       // GEMV with one row per workgroup (narrow matrices)
@@ -524,6 +531,7 @@ struct Int8Plan {
     int mtiles, ntiles, ksplit, kslice;
     size_t pstride;      // floats per split in the partials (T * N rounded up to 4)
     size_t part_bytes;   // fp32 split-K partials (workspace)
+    bool wide;           // fused variant: matrix-core GEMV with whole-line loads (5..16 tokens)
     bool kwaves;         // fused variant: K over the waves of a workgroup
 };
 Int8Plan int8_plan(int T, int N, int K, int G);
@@ -546,6 +554,9 @@ struct Int8Epilogue {
 Int8Plan int8_fused_plan(int T, int N, int K, int G);
 hipError_t launch_int8_short_fused(const uint16_t *x, const int32_t *wq, const uint16_t *ws, int T, int N, int K,
                                   int G, const Int8Epilogue &e, hipStream_t st);
+size_t int8_gemv_wide_lds(int T, int K);
+hipError_t launch_int8_gemv_wide(const uint16_t *x, const int32_t *wq, const uint16_t *ws, int T, int N, int K, int G,
+                                 const Int8Epilogue &e, hipStream_t st);
 hipError_t launch_int8_ksplit(const uint16_t *x, const int32_t *wq, const uint16_t *ws, int T, int N, int K, int G,
                               const Int8Epilogue &e, int ksplit, float *part, size_t pstride, hipStream_t st);
 hipError_t launch_int8_linear_fused(const uint16_t *x, const int32_t *wq, const uint16_t *ws, int T, int N,

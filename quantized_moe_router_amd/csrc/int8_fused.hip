@@ -24,7 +24,7 @@ struct FusedArgs {
     const uint16_t *ws;       // bf16 [N][K/G]
     int T, N, K, gshift;
     int mtiles, ntiles;
-    int mstep;                // short K: workgroups per weight-row tile
+    int mstep;                // short K: workgroups per weight-row tile; wide GEMV: waves per row block
     float *part;              // fp32 [K splits][pstride], or null
     size_t pstride;
     Int8Epilogue e;
@@ -32,10 +32,10 @@ struct FusedArgs {
 
 // ---------------------------------------------------------------------------
 // Short K: a workgroup keeps 128 weight rows (32 per wave, all of K in
-// registers) and takes one 64-token tile after the other.  The next tile's
-// activations and the present one's residual are on their way while the MFMAs
-// run.  The sums pass through LDS, so that a lane's accesses to residual and
-// out are 8 or 16 bytes wide and a row's lanes consecutive: one or two
+// registers) and takes one 64-token tile after the other; three workgroups to
+// a CU cover each other's waits.  The residual is on its way while the sums
+// pass through LDS, which they do so that a lane's accesses to residual
+// and out are 8 or 16 bytes wide and a row's lanes consecutive: one or two
 // elements per lane straight from the accumulators issue four to eight times
 // the memory instructions (8192 tokens, N = 10240, K = 320, bf16 out and
 // residual: 118 us against 142 and 173).  What bounds it: with fp32 out and
@@ -388,6 +388,184 @@ __global__ __launch_bounds__(64 * kKwWaves) void int8_ksplit_kernel(FusedArgs g)
     }
 }
 
+// ---------------------------------------------------------------------------
+// 5 to 16 tokens on wide matrices (lm_head): one read of the weights at the
+// memory's rate.  A wave owns 16 weight rows at a time.  Per step of 128 inputs
+// eight lanes load the 128 consecutive bytes of a row, and the 16 x 128 block
+// passes through LDS of the wave's own into the B operand of
+// v_mfma_f32_16x16x32_f16 (column = weight row, lane % 16; the A operand is
+// the activations, fp16 in LDS, row = token).  kGwAhead steps are on their
+// way, across row blocks.  Rows past T repeat the last token and are never
+// stored.
+//
+// What bounds it: memory, 248320 x 2560 at 8 tokens in 114 us (5.7 TB/s of
+// 654 MB); loads that put 16 rows of 64 bytes into one instruction reach 4.2.
+// Six steps ahead need more registers than two workgroups per CU have: 113 us
+// with one of them, and 20 us instead of 14 for 10240 x 2560.
+// ---------------------------------------------------------------------------
+constexpr int kGwWaves = 8, kGwThreads = 64 * kGwWaves;
+constexpr int kGwRows = 16;
+constexpr int kGwStep = kInt8WideStep;
+constexpr int kGwAhead = kInt8WideAhead;
+constexpr int kGwPitch = kGwStep + 16;   // bytes per staged row
+constexpr int kGwScGroups = 16;          // scale groups staged at a time
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2w_t __attribute__((ext_vector_type(2)));
+
+template <int G>
+__global__ __launch_bounds__(kGwThreads, 4) void int8_gemv_wide_kernel(FusedArgs g)
+{
+    constexpr int GPS = kGwStep / G;   // scale groups per step
+    __shared__ __align__(16) unsigned char s_w[kGwWaves][kGwRows * kGwPitch];
+    __shared__ uint16_t s_scale[kGwWaves][kGwScGroups * kGwRows];
+    extern __shared__ u32x4_t s_xv[];   // [T][K / 8 + 1]: one unit of padding per row
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // ks waves share a row block, each with a range of its steps (more than
+    // one: every wave has at most one block)
+    const int ks = g.mstep, part = wave % ks;
+    const int first = (blockIdx.x * kGwWaves + wave) / ks, waves = gridDim.x * kGwWaves / ks;
+    const int nrb = (g.N + kGwRows - 1) / kGwRows, groups = g.K / G;
+    const int s0 = part * (g.K / kGwStep) / ks, steps = (part + 1) * (g.K / kGwStep) / ks - s0;
+    const int blocks = first < nrb ? (nrb - first + waves - 1) / waves : 0;
+    const int U = blocks * steps;
+
+    // load cursor: step s0 + lst of row block lb; past the last unit it stays
+    int lb = 0, lst = 0;
+    const char *wb = nullptr;
+    uint32_t wo[2];
+    auto aim = [&]() {
+        const int row0 = (first + lb * waves) * kGwRows;
+        wb = reinterpret_cast<const char *>(g.wq) + (size_t)row0 * g.K + (size_t)s0 * kGwStep;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            wo[i] = min(8 * i + (lane >> 3), g.N - 1 - row0) * (uint32_t)g.K + 16 * (lane & 7);
+    };
+    struct Raw {
+        u32x4_t w[2];
+    };
+    auto load_next = [&](Raw &r) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            r.w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(wb + (wo[i] + (uint32_t)(kGwStep * lst))));
+        if (lst + 1 < steps) {
+            ++lst;
+        } else if (lb + 1 < blocks) {
+            lst = 0;
+            ++lb;
+            aim();
+        }
+    };
+    // scales of the groups from s0 GPS + grp on of block b, 16 lanes on those of a row
+    uint32_t sv[4];
+    auto load_scales = [&](int b, int grp) {
+        const int row0 = (first + b * waves) * kGwRows;
+        const uint16_t *sb = g.ws + (size_t)row0 * groups;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            sv[i] = sb[min(4 * i + (lane >> 4), g.N - 1 - row0) * (uint32_t)groups +
+                       min(s0 * GPS + grp + (lane & 15), groups - 1)];
+    };
+    Raw raw[kGwAhead];
+    if (U > 0) {
+        aim();
+        load_scales(0, 0);
+#pragma unroll
+        for (int q = 0; q < kGwAhead; ++q) load_next(raw[q]);
+    }
+    const int K8 = g.K >> 3, xs = K8 + 1;
+    for (int i = tid; i < g.T * K8; i += kGwThreads) {
+        const int t = i / K8, c = i - t * K8;
+        s_xv[t * xs + c] = bf16x8_to_f16x8(*reinterpret_cast<const u32x4_t *>(g.x + t * g.e.x_stride + 8 * c));
+    }
+    __syncthreads();
+
+    const int n = lane & 15, kq = lane >> 4;
+    const u32x4_t *xrow = s_xv + min(n, g.T - 1) * xs + kq + s0 * (kGwStep / 8);
+    uint16_t *s_sc = s_scale[wave];   // [group][row]
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    int cb = 0, cst = 0;
+    // a finished block's sums and its number, until the epilogue comes round
+    // (one copy of it, between runs of kGwAhead steps: no two blocks end in one)
+    f32x4_t done = acc;
+    int db = -1;
+    auto compute = [&](Raw &r) {
+        const int grp = cst * GPS;
+        if (grp % kGwScGroups == 0) {   // this chunk of scales to LDS, the next on its way
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s_sc[(lane & 15) * kGwRows + 4 * i + (lane >> 4)] = (uint16_t)sv[i];
+            const bool more = grp + kGwScGroups < steps * GPS;
+            load_scales(more ? cb : min(cb + 1, blocks - 1), more ? grp + kGwScGroups : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<u32x4_t *>(s_w[wave] + (8 * i + (lane >> 3)) * kGwPitch + 16 * (lane & 7)) = r.w[i];
+        load_next(r);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        f32x4_t tmp = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const u32x2w_t w = *reinterpret_cast<const u32x2w_t *>(s_w[wave] + n * kGwPitch + 32 * m + 8 * kq);
+            const uint32_t wa = w[0], wc = w[1];
+            const h2_t p0 = code_pair<0>(wa), p1 = code_pair<1>(wa);
+            const h2_t p2 = code_pair<0>(wc), p3 = code_pair<1>(wc);
+            const f16x8_t bf = {p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+            const u32x4_t xv = xrow[cst * (kGwStep / 8) + 4 * m];
+            tmp = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, xv), bf, tmp, 0, 0, 0);
+            if (GPS == 1 ? m == 3 : m & 1) {
+                const float sf = bf16_to_f32(s_sc[(grp + (GPS == 2 ? m >> 1 : 0)) % kGwScGroups * kGwRows + n]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    acc[j] = fmaf(sf, tmp[j], acc[j]);
+                    tmp[j] = 0.f;
+                }
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (++cst == steps) {
+            done = acc;
+            db = cb;
+            acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            cst = 0;
+            ++cb;
+        }
+        __builtin_amdgcn_sched_barrier(0);   // nothing of the next step: its data would be waited for
+    };
+    auto store = [&]() {   // the lane holds tokens 4 kq + j of row n
+        int nn = n, t0 = 4 * kq;
+        asm volatile("" : "+v"(nn), "+v"(t0));   // the addresses are made here, not kept in registers all along
+        const int row = (first + db * waves) * kGwRows + nn;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (t0 + j < g.T && row < g.N) finish(g.e, t0 + j, row, done[j]);
+        db = -1;
+    };
+    for (int u = 0; u < U; u += kGwAhead) {
+        if (u + kGwAhead <= U) {
+#pragma unroll
+            for (int q = 0; q < kGwAhead; ++q) compute(raw[q]);
+        } else {
+#pragma unroll
+            for (int q = 0; q < kGwAhead; ++q)
+                if (u + q < U) compute(raw[q]);
+        }
+        if (ks == 1 && db >= 0) store();
+    }
+    if (ks > 1) {   // the waves' sums, in wave order
+        float *sums = reinterpret_cast<float *>(s_w[wave]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sums[4 * lane + j] = done[j];
+        __syncthreads();
+        if (part == 0 && blocks > 0) {
+            for (int w = 1; w < ks; ++w)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) done[j] += reinterpret_cast<const float *>(s_w[wave + w])[4 * lane + j];
+            store();
+        }
+    }
+}
+
 template <int RES>
 void launch_short(const FusedArgs &a, int grid, hipStream_t st)
 {
@@ -427,6 +605,32 @@ hipError_t launch_int8_short_fused(const uint16_t *x, const int32_t *wq, const u
     if (!e.residual) launch_short<0>(a, grid, st);
     else if (e.residual_type == kF32) launch_short<4>(a, grid, st);
     else launch_short<2>(a, grid, st);
+    return hipGetLastError();
+}
+
+size_t int8_gemv_wide_lds(int T, int K) { return (size_t)T * (K / 8 + 1) * 16; }
+
+hipError_t launch_int8_gemv_wide(const uint16_t *x, const int32_t *wq, const uint16_t *ws, int T, int N, int K, int G,
+                                 const Int8Epilogue &e, hipStream_t st)
+{
+    FusedArgs a = fused_args(x, wq, ws, T, N, K, G, e, 16, kGwRows);
+    // two workgroups to a CU (one where the activations take most of its LDS),
+    // with the same number of row blocks per wave; fewer blocks than waves are
+    // shared out
+    const size_t lds = int8_gemv_wide_lds(T, K);
+    const int most = (lds <= 57344 ? 2 : 1) * 256 * kGwWaves, turns = (a.ntiles + most - 1) / most;
+    a.mstep = 1;
+    while (turns == 1 && 2 * a.mstep <= kGwWaves && 2 * a.mstep * a.ntiles <= most && 2 * a.mstep * kGwStep <= K)
+        a.mstep *= 2;
+    const int grid = (a.ntiles * a.mstep + turns * kGwWaves - 1) / (turns * kGwWaves);
+    if (lds > 65536) {
+        const void *f = G == 64 ? reinterpret_cast<const void *>(int8_gemv_wide_kernel<64>)
+                                : reinterpret_cast<const void *>(int8_gemv_wide_kernel<128>);
+        const hipError_t rc = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (rc != hipSuccess) return rc;
+    }
+    if (G == 64) int8_gemv_wide_kernel<64><<<grid, kGwThreads, lds, st>>>(a);
+    else int8_gemv_wide_kernel<128><<<grid, kGwThreads, lds, st>>>(a);
     return hipGetLastError();
 }
 

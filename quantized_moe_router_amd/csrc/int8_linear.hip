@@ -1121,7 +1121,10 @@ hipError_t launch_int8_linear(const uint16_t *x, const int32_t *wq, const uint16
     return launch_plan<false>(int8_plan(T, N, K, G), x, wq, ws, T, N, K, G, out, Int8Epilogue{}, workspace, st);
 }
 
-// The fused layer's plan: the plain one's, but for few output tiles of 32 x 32
+// The fused layer's plan: the plain one's, but 5 to 16 tokens on wide matrices
+// take the GEMV with whole-line loads (248320 x 2560: 8 tokens 114 us against
+// int8_gemv_mfma_kernel's 154, 16 tokens 121 against int8_gemm_kernel's 164),
+// and for few output tiles of 32 x 32
 // K goes over the waves of a workgroup (measured with int8_gemm_kernel's time
 // behind: N = 320, K = 10240: 32 tokens 8.1 us, 10.9; 512 tokens, 160 tiles,
 // 19.4, 21.8; 1024 tokens, 320 tiles, 36.0, 29.6; N = 1003, K = 1152: 77
@@ -1132,6 +1135,11 @@ hipError_t launch_int8_linear(const uint16_t *x, const int32_t *wq, const uint16
 Int8Plan int8_fused_plan(int T, int N, int K, int G)
 {
     Int8Plan p = int8_plan(T, N, K, G);
+    if (T > kInt8GemvMaxTokens && T <= kInt8MfmaGemvMaxTokens && (N + 3) / 4 >= kInt8GemvMaxBlocks &&
+        K % kInt8WideStep == 0 && K >= kInt8WideMinK && int8_gemv_wide_lds(T, K) <= kInt8WideMaxLds) {
+        p = Int8Plan{};
+        p.gemv = p.wide = true;
+    }
     if (p.gemv || T == 0 || p.short_k) return p;
     const long tiles = (long)((T + 31) / 32) * ((N + 31) / 32);
     if (tiles > (K <= 2560 ? 512 : 256)) return p;
@@ -1148,6 +1156,7 @@ hipError_t launch_int8_linear_fused(const uint16_t *x, const int32_t *wq, const 
                                     int K, int G, const Int8Epilogue &e, void *workspace, hipStream_t st)
 {
     const Int8Plan p = int8_fused_plan(T, N, K, G);
+    if (p.wide) return launch_int8_gemv_wide(x, wq, ws, T, N, K, G, e, st);
     if (p.short_k && e.vec) return launch_int8_short_fused(x, wq, ws, T, N, K, G, e, st);
     if (p.kwaves) {
         float *part = static_cast<float *>(workspace);

@@ -169,6 +169,17 @@ CASES = [
     (16, 2001, 320, 64, "fp32", "gelu_tanh", "fp16", "fp16", True),
     (12, 8200, 2560, 128, "fp16", "none", None, "fp32", False),
     (5, 320, 10240, 64, "bf16", "silu", None, "bf16", False),
+    (5, 8189, 512, 64, "bf16", "silu", "fp16", "fp32", True),
+    (6, 8200, 640, 64, None, "gelu", "bf16", "fp16", False),
+    (9, 33001, 768, 128, "fp32", "none", "fp32", "fp32", True),
+    (13, 70000, 512, 64, None, "relu", None, "bf16", False),
+    (16, 8192, 2560, 128, "bf16", "none", "bf16", "fp32", False),
+    (8, 8190, 4096, 64, None, "sigmoid", None, "fp32", False),
+    (16, 66000, 256, 64, None, "none", None, "fp32", False),
+    (7, 10240, 320, 64, None, "none", "bf16", "bf16", False),
+    (11, 8195, 4224, 64, "bf16", "none", "bf16", "fp32", True),
+    (40, 77, 8192, 64, "bf16", "silu", "bf16", "fp32", True),
+    (300, 40, 16384, 128, None, "silu", "fp16", "fp16", False),
     (6, 320, 2048, 64, "bf16", "silu", "bf16", "bf16", False),
     (9, 317, 2048, 64, "bf16", "silu", "fp32", "fp32", True),
     (16, 33, 4096, 128, None, "relu", "fp16", "fp32", False),
@@ -281,6 +292,7 @@ def test_fused_infinities_nan_and_fp16_overflow(T, N, K):
 
 
 @pytest.mark.parametrize("T,N,K,G", [(1, 320, 10240, 64), (3, 4100, 320, 64), (8, 9001, 1152, 128), (9, 320, 10240, 64),
+                                     (16, 8200, 2560, 128), (5, 40000, 512, 64), (2000, 256, 1024, 64),
                                      (512, 320, 10240, 64), (100, 10240, 320, 64), (70, 1000, 1152, 128)])
 def test_fused_graph_replay_and_another_stream(T, N, K, G):
     label = f"graph T={T} N={N} K={K}"
