@@ -522,6 +522,7 @@ constexpr int kInt8WideStep = 128;
 constexpr int kInt8WideAhead = 4;
 constexpr int kInt8WideMinK = kInt8WideStep * kInt8WideAhead;
 constexpr size_t kInt8WideMaxLds = 136 * 1024;
+constexpr long kInt8WideMinWeights = 1L << 26;   // from so many weights on also for 3 and 4 tokens
 
 struct Int8Plan {
     bool gemv;

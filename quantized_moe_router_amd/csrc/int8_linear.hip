@@ -1124,7 +1124,9 @@ hipError_t launch_int8_linear(const uint16_t *x, const int32_t *wq, const uint16
 // The fused layer's plan: the plain one's, but 5 to 16 tokens on wide matrices
 // take the GEMV with whole-line loads (248320 x 2560: 8 tokens 114 us against
 // int8_gemv_mfma_kernel's 154, 16 tokens 121 against int8_gemm_kernel's 164),
-// and for few output tiles of 32 x 32
+// on large ones from 3 tokens (4 tokens: 248320 x 2560 107 us against
+// int8_gemv_kernel's 136, 32000 x 4096 28 against 33, but 10240 x 2560 13
+// against 11; 2 tokens gain nothing), and for few output tiles of 32 x 32
 // K goes over the waves of a workgroup (measured with int8_gemm_kernel's time
 // behind: N = 320, K = 10240: 32 tokens 8.1 us, 10.9; 512 tokens, 160 tiles,
 // 19.4, 21.8; 1024 tokens, 320 tiles, 36.0, 29.6; N = 1003, K = 1152: 77
@@ -1135,7 +1137,8 @@ hipError_t launch_int8_linear(const uint16_t *x, const int32_t *wq, const uint16
 Int8Plan int8_fused_plan(int T, int N, int K, int G)
 {
     Int8Plan p = int8_plan(T, N, K, G);
-    if (T > kInt8GemvMaxTokens && T <= kInt8MfmaGemvMaxTokens && (N + 3) / 4 >= kInt8GemvMaxBlocks &&
+    const int from = (long)N * K >= kInt8WideMinWeights ? 3 : kInt8GemvMaxTokens + 1;
+    if (T >= from && T <= kInt8MfmaGemvMaxTokens && (N + 3) / 4 >= kInt8GemvMaxBlocks &&
         K % kInt8WideStep == 0 && K >= kInt8WideMinK && int8_gemv_wide_lds(T, K) <= kInt8WideMaxLds) {
         p = Int8Plan{};
         p.gemv = p.wide = true;

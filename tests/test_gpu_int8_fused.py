@@ -170,6 +170,8 @@ CASES = [
     (12, 8200, 2560, 128, "fp16", "none", None, "fp32", False),
     (5, 320, 10240, 64, "bf16", "silu", None, "bf16", False),
     (5, 8189, 512, 64, "bf16", "silu", "fp16", "fp32", True),
+    (3, 131072, 512, 64, "bf16", "none", None, "bf16", False),
+    (4, 33000, 2048, 128, None, "silu", "bf16", "fp32", True),
     (6, 8200, 640, 64, None, "gelu", "bf16", "fp16", False),
     (9, 33001, 768, 128, "fp32", "none", "fp32", "fp32", True),
     (13, 70000, 512, 64, None, "relu", None, "bf16", False),
