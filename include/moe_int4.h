@@ -300,10 +300,11 @@ typedef struct moe_int8_epilogue {
  *   out  [tokens][n] of out_type, rows out_stride >= n elements apart; what
  *        lies between the rows is left as it was
  *   epilogue  may be NULL (out is then the plain product)
- * With one token the strides are not read.  x, w_packed and w_scales are
- * 16-byte aligned; bias, residual and out need the alignment of their
- * elements only.  out must not overlap x or bias; it may be the residual
- * itself (same address, type and stride), and must not overlap it otherwise.
+ * Strides are at most 2^24 elements; with one token they are not read.  x,
+ * w_packed and w_scales are 16-byte aligned; bias, residual and out need the
+ * alignment of their elements only.  out must not overlap x, the weights or
+ * the bias; it may be the residual itself (same address, type and stride), and
+ * must not overlap it otherwise.
  * Shapes, activations and determinism as in moe_int8_linear.  The workspace
  * (moe_int8_linear_fused_workspace_bytes; NULL when that is 0) needs no
  * clearing and holds nothing between calls; calls in flight at the same time
@@ -369,7 +370,8 @@ typedef struct moe_int4_logits_rules {
  *           themselves (same address, type and stride) and must not overlap
  *           them otherwise, nor any of the rules' tables.
  * rows in [0, 65536] (0 is a no-op), vocab in [1, 2^24], rows * vocab below
- * 2^34, widths in [0, 2^24].
+ * 2^34, widths in [0, 2^24], strides at most 2^24; with one row they are not
+ * read.
  * Pointers need the alignment of their elements only.  Needs no workspace.
  * The result does not depend on the order in which the history is counted.
  * The stream must belong to the current device. */

@@ -272,6 +272,16 @@ def device_index(t, name: str, index: int | None = None) -> int:
     return i
 
 
+def _current_device() -> int:
+    import torch
+    return torch.cuda.current_device()
+
+
+def _device(index: int):
+    import torch
+    return torch.cuda.device(index)
+
+
 def _stream_on(stream, index: int) -> int | None:
     """The given stream, or torch's current one on a device (its handle alone:
     building the stream object costs as much as a launch's other checks)."""
@@ -310,6 +320,10 @@ def moe_int8_linear_fused(x, w_packed, w_scales, tokens: int, n: int, k: int, gr
         e.residual_stride = row_stride(residual, "residual", tokens, n)
         e.residual, e.residual_type = residual.data_ptr(), type_code(residual.dtype)
     index = device_index(x, "x")
+    if index != _current_device():   # its stream, and its device for the launch
+        with _device(index):
+            return moe_int8_linear_fused(x, w_packed, w_scales, tokens, n, k, group, out, bias, residual, activation,
+                                         workspace, stream)
     for name, t in (("w_packed", w_packed), ("w_scales", w_scales), ("out", out), ("bias", bias),
                     ("residual", residual), ("workspace", workspace)):
         if t is not None:
@@ -334,6 +348,9 @@ def moe_int4_logits_process(logits, rules: MoeLogitsRules, out, stream=None):
     in_type, out_type = type_code(logits.dtype), type_code(out.dtype)
     index = device_index(logits, "logits")
     device_index(out, "out", index)
+    if index != _current_device():
+        with _device(index):
+            return moe_int4_logits_process(logits, rules, out, stream)
     rc = lib().moe_int4_logits_process(logits.data_ptr(), in_type, stride, rows, vocab, ctypes.byref(rules),
                                        out.data_ptr(), out_type, out_stride, _stream_on(stream, index))
     if rc:

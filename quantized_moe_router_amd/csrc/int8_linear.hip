@@ -122,10 +122,10 @@ __global__ __launch_bounds__(kGvThreads) void int8_gemv_kernel(const uint16_t *_
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const uint32_t e = v[q];
-                sum = __builtin_amdgcn_fdot2(__builtin_bit_cast(h2_t, e), one, sum, false);
+                if (!F) sum = __builtin_amdgcn_fdot2(__builtin_bit_cast(h2_t, e), one, sum, false);
             }
         }
-        s_xsum[t * CPR + c] = sum;
+        if (!F) s_xsum[t * CPR + c] = sum;
     }
     __syncthreads();
 
@@ -170,7 +170,7 @@ __global__ __launch_bounds__(kGvThreads) void int8_gemv_kernel(const uint16_t *_
         float xsum[T];
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            xsum[t] = s_xsum[t * CPR + c];
+            if (!F) xsum[t] = s_xsum[t * CPR + c];
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 const u32x4_t v = s_x[(t * 2 + p) * CPR + c];
@@ -188,6 +188,9 @@ __global__ __launch_bounds__(kGvThreads) void int8_gemv_kernel(const uint16_t *_
             h2_t cp[8];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
+                // fused: the bias comes off every code.  Taken off once per chunk it
+                // leaves the sum's rounding at 1024 times x, which a bf16 output
+                // hides and an fp32 one does not
                 cp[2 * q] = F ? code_pair<0>(r.w[j][q]) : code_pair_biased<0>(r.w[j][q]);
                 cp[2 * q + 1] = F ? code_pair<1>(r.w[j][q]) : code_pair_biased<1>(r.w[j][q]);
             }

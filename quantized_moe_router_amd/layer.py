@@ -95,10 +95,6 @@ class Int8Linear:
                 out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
         """residual + act(x W^T + bias) on torch's current stream of x's
         device; x bf16 [tokens, k].  out may be the residual."""
-        index = x.get_device()
-        if index >= 0 and index != torch.cuda.current_device():
-            with torch.cuda.device(index):
-                return self.forward(x, residual, out, out_dtype)
         tokens = x.shape[0]
         if out is None:
             out = torch.empty(tokens, self.n, dtype=out_dtype, device=x.device)
@@ -187,10 +183,7 @@ class LogitsRules:
         if logits.dim() != 2 or logits.shape[1] != self.vocab or (self.rows is not None
                                                                   and logits.shape[0] > self.rows):
             raise ValueError(f"logits is {tuple(logits.shape)}, expected at most {self.rows} rows of {self.vocab}")
-        index = B.device_index(logits, "logits", self._index)
-        if index != torch.cuda.current_device():
-            with torch.cuda.device(index):
-                return self.apply(logits, out, out_dtype)
+        B.device_index(logits, "logits", self._index)
         if out is None:
             out = torch.empty(logits.shape, dtype=out_dtype, device=logits.device)
         B.moe_int4_logits_process(logits, self._c, out)

@@ -54,6 +54,9 @@ FINE = "a valid call"   # stops only where there is no gfx950 device; not made w
     (dict(os_=1 << 41), B.EINVAL, "out: stride"),
     (dict(out=FAKE), B.EINVAL, "out overlaps x"),
     (dict(out=FAKE + 2 * 3 * 2560 + 100), B.EINVAL, "out overlaps x"),
+    (dict(out=FAKE * 2 + 1000), B.EINVAL, "out overlaps w_packed"),
+    (dict(out=FAKE * 3 + 64), B.EINVAL, "out overlaps w_scales"),
+    (dict(tokens=64, k=10240, xs=10240, n=96, os_=96, ws=FAKE * 4 + 64), B.EINVAL, "workspace overlaps"),
     (dict(epi=dict(activation=6)), B.EINVAL, "activation 6"),
     (dict(epi=dict(activation=-1)), B.EINVAL, "activation -1"),
     (dict(epi=dict(bias=FAKE * 5, bias_type=7)), B.EINVAL, "bias: type 7"),
@@ -63,9 +66,9 @@ FINE = "a valid call"   # stops only where there is no gfx950 device; not made w
     (dict(epi=dict(residual=FAKE * 5, residual_type=F32, residual_stride=0)), B.EINVAL, "residual: stride 0"),
     (dict(epi=dict(residual=FAKE * 4, residual_type=F16, residual_stride=320)), B.EINVAL, "out overlaps residual"),
     (dict(epi=dict(residual=FAKE * 4 + 320, residual_type=BF16, residual_stride=320)), B.EINVAL, "out overlaps residual"),
-    (dict(tokens=512, ws=None), B.EINVAL, "workspace is NULL"),
-    (dict(tokens=512, ws=FAKE * 8 + 4), B.EALIGN, "workspace is not"),
-    (dict(tokens=512, wb=1024), B.EWORKSPACE, "workspace has 1024"),
+    (dict(tokens=64, k=10240, xs=10240, ws=None), B.EINVAL, "workspace is NULL"),
+    (dict(tokens=64, k=10240, xs=10240, ws=FAKE * 8 + 4), B.EALIGN, "workspace is not"),
+    (dict(tokens=64, k=10240, xs=10240, wb=1024), B.EWORKSPACE, "workspace has 1024"),
     # fine up to the device check
     (dict(), B.EDEVICE, FINE),
     (dict(tokens=1, xs=0, os_=0), B.EDEVICE, FINE),
@@ -89,7 +92,8 @@ def test_fused_zero_tokens_and_workspace_query():
     b = ctypes.c_size_t(1)
     q = B.lib().moe_int8_linear_fused_workspace_bytes
     assert q(1, 248320, 2560, 128, ctypes.byref(b)) == 0 and b.value == 0
-    assert q(512, 320, 10240, 64, ctypes.byref(b)) == 0 and b.value > 0
+    assert q(512, 320, 10240, 64, ctypes.byref(b)) == 0 and b.value == 0   # K over waves, whose sums meet in LDS
+    assert q(64, 320, 10240, 64, ctypes.byref(b)) == 0 and b.value > 0     # and over workgroups
     assert q(512, 320, 10240, 65, ctypes.byref(b)) == B.EINVAL
     assert q(512, 320, 10240, 64, None) == B.EINVAL
 
