@@ -38,54 +38,18 @@ __device__ __forceinline__ u32x4_t bf16x8_to_f16x8(u32x4_t v)
 // exp, erfc and the division are the accurate ones: an fp32 output shows
 // errors that a bf16 one would hide.
 // ---------------------------------------------------------------------------
-template <int KIND>
-__device__ __forceinline__ float activate_as(float v)
+// One body for the three that divide by 1 + e^z: kernels of a few microseconds
+// fetch their code anew at every launch, and a copy of every activation per
+// output cost the short-K kernel more than its products.
+__device__ __forceinline__ float activate(float v, int kind)   // kind is uniform over the launch
 {
-    if constexpr (KIND == kActRelu) return v < 0.f ? 0.f : v;   // a NaN passes
-    if constexpr (KIND == kActSilu) return v / (1.f + expf(-v));
-    if constexpr (KIND == kActGelu) return 0.5f * v * erfcf(-0.70710678118654752f * v);
-    if constexpr (KIND == kActGeluTanh) {
-        // 0.5 (1 + tanh u) = 1 / (1 + e^-2u), without tanh's cancellation near -1
-        const float u = 0.79788456080286536f * fmaf(0.044715f * v * v, v, v);
-        return v / (1.f + expf(-2.f * u));
-    }
-    if constexpr (KIND == kActSigmoid) return 1.f / (1.f + expf(-v));
-    return v;
-}
-
-// M values at a time; the kind is uniform over the launch.
-template <int M>
-__device__ __forceinline__ void activate(float (&v)[M], int kind)
-{
-    switch (kind) {
-    case kActRelu:
-#pragma unroll
-        for (int i = 0; i < M; ++i) v[i] = activate_as<kActRelu>(v[i]);
-        break;
-    case kActSilu:
-#pragma unroll
-        for (int i = 0; i < M; ++i) v[i] = activate_as<kActSilu>(v[i]);
-        break;
-    case kActGelu:
-#pragma unroll
-        for (int i = 0; i < M; ++i) v[i] = activate_as<kActGelu>(v[i]);
-        break;
-    case kActGeluTanh:
-#pragma unroll
-        for (int i = 0; i < M; ++i) v[i] = activate_as<kActGeluTanh>(v[i]);
-        break;
-    case kActSigmoid:
-#pragma unroll
-        for (int i = 0; i < M; ++i) v[i] = activate_as<kActSigmoid>(v[i]);
-        break;
-    default: break;
-    }
-}
-__device__ __forceinline__ float activate(float v, int kind)
-{
-    float a[1] = {v};
-    activate(a, kind);
-    return a[0];
+    if (kind == kActNone) return v;
+    if (kind == kActRelu) return v < 0.f ? 0.f : v;   // a NaN passes
+    if (kind == kActGelu) return 0.5f * v * erfcf(-0.70710678118654752f * v);
+    float z = -v;
+    // 0.5 (1 + tanh u) = 1 / (1 + e^-2u), without tanh's cancellation near -1
+    if (kind == kActGeluTanh) z = -2.f * 0.79788456080286536f * fmaf(0.044715f * v * v, v, v);
+    return (kind == kActSigmoid ? 1.f : v) / (1.f + expf(z));
 }
 
 __device__ __forceinline__ void finish(const Int8Epilogue &e, int t, int r, float v)
@@ -103,8 +67,9 @@ __device__ __forceinline__ void finish4(const Int8Epilogue &e, int t, int r, flo
         const float4 b = load_typed4(e.bias, e.bias_type, r);
         v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
     }
-    v = make_float4(activate(v.x, e.activation), activate(v.y, e.activation), activate(v.z, e.activation),
-                    activate(v.w, e.activation));
+    if (e.activation != kActNone)
+        v = make_float4(activate(v.x, e.activation), activate(v.y, e.activation), activate(v.z, e.activation),
+                        activate(v.w, e.activation));
     if (e.residual) {
         const float4 b = load_typed4(e.residual, e.residual_type, t * e.residual_stride + r);
         v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);

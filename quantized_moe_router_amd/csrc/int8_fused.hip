@@ -115,6 +115,8 @@ __global__ __launch_bounds__(kSpThreads, 3) void int8_short_fused_kernel(FusedAr
     auto lane_offset = [&](size_t stride, int bytes) {
         return nn < g.N ? ((uint32_t)r0 * (uint32_t)stride + (uint32_t)nn) * (uint32_t)bytes : 0x80000000u;
     };
+    // the bias where no activation has taken it in
+    const float4 late = g.e.activation == kActNone ? bias : make_float4(0.f, 0.f, 0.f, 0.f);
     const int ob = type_bytes(g.e.out_type);
     const uint32_t roff = lane_offset(g.e.residual_stride, RES), rstep = 8u * (uint32_t)g.e.residual_stride * RES;
     const uint32_t ooff = lane_offset(g.e.out_stride, ob), ostep = 8u * (uint32_t)g.e.out_stride * ob;
@@ -198,6 +200,17 @@ __global__ __launch_bounds__(kSpThreads, 3) void int8_short_fused_kernel(FusedAr
         for (int j = 0; j < 16; ++j)
             s_c[(32 * mt + 8 * (j >> 2) + 4 * half + (j & 3)) * kSpCs + 32 * wave + (lane & 31)] = acc[mt][j];
     __syncthreads();
+    // an activation in place (this thread's own words), in a loop of its own:
+    // unrolled with the stores it was 25 KB of code, fetched at every launch
+    if (g.e.activation != kActNone) {
+#pragma unroll 1
+        for (int u = 0; u < kSpM / 8; ++u) {
+            float4 *w = reinterpret_cast<float4 *>(s_c + (8 * u + r0) * kSpCs + c4);
+            const float4 f = *w;
+            *w = make_float4(activate(f.x + bias.x, g.e.activation), activate(f.y + bias.y, g.e.activation),
+                             activate(f.z + bias.z, g.e.activation), activate(f.w + bias.w, g.e.activation));
+        }
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         if (32 * h >= rows) break;
@@ -205,8 +218,7 @@ __global__ __launch_bounds__(kSpThreads, 3) void int8_short_fused_kernel(FusedAr
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const float4 f = *reinterpret_cast<const float4 *>(s_c + (32 * h + 8 * u + r0) * kSpCs + c4);
-            float v[4] = {f.x + bias.x, f.y + bias.y, f.z + bias.z, f.w + bias.w};
-            activate(v, g.e.activation);
+            float v[4] = {f.x + late.x, f.y + late.y, f.z + late.z, f.w + late.w};
             const u32x4_t w = res[4 * h + u];
             if constexpr (RES == 4) {
 #pragma unroll

@@ -698,6 +698,7 @@ __global__ __launch_bounds__(kGmThreads, 2) void int8_gemm_kernel(Int8GemmArgs g
                     acc[2 * hp + u][j];
         }
         __syncthreads();
+#pragma unroll 1
         for (int it = tid; it < 64 * (kGmN / 4); it += kGmThreads) {
             const int r = it / (kGmN / 4), c4 = 4 * (it % (kGmN / 4));
             const int m = 64 * hp + r, nn = n0 + c4;
@@ -873,6 +874,7 @@ __global__ __launch_bounds__(kGoThreads, 1) void int8_gemm_short_kernel(Int8Gemm
                     acc[2 * hp + u][j];
         }
         __syncthreads();
+#pragma unroll 1
         for (int it = tid; it < 64 * (kGoN / 4); it += kGoThreads) {
             const int r = it / (kGoN / 4), c4 = 4 * (it % (kGoN / 4));
             const int m = 64 * hp + r, nn = n0 + c4;
