@@ -35,10 +35,32 @@ __device__ __forceinline__ u32x4_t bf16x8_to_f16x8(u32x4_t v)
 //   out[t][r] = rnd(residual[t][r] + act(sum + bias[r]))
 // in fp32, one rounding.  Everything happens on the sum in registers, so the
 // activation and the addition cost no pass over [T][N] of their own.
-// exp, erfc and the division are the accurate ones: an fp32 output shows
-// errors that a bf16 one would hide.
+// Accurate to a few units of fp32's last place throughout: an fp32 output
+// shows errors that a bf16 one would hide.
 // ---------------------------------------------------------------------------
-// One body for the three that divide by 1 + e^z: kernels of a few microseconds
+// 1 / (1 + e^-z), as t / (1 + t) or 1 / (1 + t) with t = e^-|z| in (0, 1]: no
+// overflow, and a divisor in [1, 2], whose reciprocal is the hardware's with
+// one Newton step.  t is 2^h (1 + r ln 2) with h = fp32(-|z| log2 e) and r what
+// h leaves of the product (the hardware's exponential alone, on the rounded
+// product, is off by |z| units of the last place).  Half the instructions of
+// expf and a division: 512 tokens of a [10240, 320] layer with SiLU and a
+// residual 18.7 us against 20.2, 2048 of [4096, 2560] 73.8 against 74.9.
+// Below fp32's normal range t is zero.
+__device__ __forceinline__ float sigmoid(float z)
+{
+    constexpr float kL = 1.44269504088896341f;           // log2 e as fp32, and the rest of it
+    constexpr float kLr = (float)(1.44269504088896340736 - (double)kL);
+    const float a = -fabsf(z), h = a * kL;
+    const float r = fmaf(a, kL, -h) + a * kLr;
+    float t = __builtin_amdgcn_exp2f(h);
+    t = h < -126.f ? 0.f : fmaf(t * 0.69314718055994531f, r, t);   // -inf, too, whose r is not a number
+    const float d = 1.f + t;
+    float q = __builtin_amdgcn_rcpf(d);
+    q = fmaf(fmaf(-d, q, 1.f), q, q);
+    return z < 0.f ? t * q : q;   // a NaN passes through t
+}
+
+// One body for the three that hold a sigmoid: kernels of a few microseconds
 // fetch their code anew at every launch, and a copy of every activation per
 // output cost the short-K kernel more than its products.
 __device__ __forceinline__ float activate(float v, int kind)   // kind is uniform over the launch
@@ -46,10 +68,10 @@ __device__ __forceinline__ float activate(float v, int kind)   // kind is unifor
     if (kind == kActNone) return v;
     if (kind == kActRelu) return v < 0.f ? 0.f : v;   // a NaN passes
     if (kind == kActGelu) return 0.5f * v * erfcf(-0.70710678118654752f * v);
-    float z = -v;
-    // 0.5 (1 + tanh u) = 1 / (1 + e^-2u), without tanh's cancellation near -1
-    if (kind == kActGeluTanh) z = -2.f * 0.79788456080286536f * fmaf(0.044715f * v * v, v, v);
-    return (kind == kActSigmoid ? 1.f : v) / (1.f + expf(z));
+    float z = v;
+    // 0.5 (1 + tanh u) = sigmoid(2 u), without tanh's cancellation near -1
+    if (kind == kActGeluTanh) z = 2.f * 0.79788456080286536f * fmaf(0.044715f * v * v, v, v);
+    return (kind == kActSigmoid ? 1.f : v) * sigmoid(z);
 }
 
 __device__ __forceinline__ void finish(const Int8Epilogue &e, int t, int r, float v)

@@ -72,8 +72,9 @@ def act64(v, kind):
         a, amp = sigmoid(v), 0.0
     else:
         return v, np.zeros_like(v)
-    # results below fp32's normal range have its subnormal step
-    return a, (16 + amp) * U * np.abs(a) + 2.0 ** -126
+    # a sigmoid below fp32's normal range, 2^-126, comes out as zero: that much
+    # of the factor v, and of the result itself where there is none
+    return a, (16 + amp) * U * np.abs(a) + 2.0 ** -126 * np.maximum(np.abs(v), 1)
 
 
 def inside(t, extra, fill):
