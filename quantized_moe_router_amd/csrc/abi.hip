@@ -683,10 +683,10 @@ int32_t moe_int8_linear_fused(const uint16_t *x, int64_t x_stride, const int32_t
     if (tokens > 1 && x_stride % 8)
         return fail(MOE_INT4_EALIGN, "x: stride %lld is not a multiple of 8", (long long)x_stride);
     if (may_overlap(rx, ro)) return fail(MOE_INT4_EINVAL, "out overlaps x");
-    if (may_overlap({"w_packed", w_packed, MOE_TYPE_F32, 0, 1, (int64_t)n * (k / 4)}, ro))
-        return fail(MOE_INT4_EINVAL, "out overlaps w_packed");
-    if (may_overlap({"w_scales", w_scales, MOE_TYPE_BF16, 0, 1, (int64_t)n * (k / group)}, ro))
-        return fail(MOE_INT4_EINVAL, "out overlaps w_scales");
+    const Rows rp{"w_packed", w_packed, MOE_TYPE_F32, 0, 1, (int64_t)n * (k / 4)};
+    const Rows rs{"w_scales", w_scales, MOE_TYPE_BF16, 0, 1, (int64_t)n * (k / group)};
+    if (may_overlap(rp, ro)) return fail(MOE_INT4_EINVAL, "out overlaps w_packed");
+    if (may_overlap(rs, ro)) return fail(MOE_INT4_EINVAL, "out overlaps w_scales");
     bool vec = n % 4 == 0 && rows_aligned(ro, 4);
     if (e.bias) {
         if ((rc = check_rows(rb))) return rc;
@@ -705,11 +705,11 @@ int32_t moe_int8_linear_fused(const uint16_t *x, int64_t x_stride, const int32_t
         if (!aligned16(workspace)) return fail(MOE_INT4_EALIGN, "workspace is not 16-byte aligned");
         if (workspace_bytes < need)
             return fail(MOE_INT4_EWORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
-        // the partial sums are written before x's and the residual's last reads
+        // the partial sums are written before the inputs' last reads
         const Rows rw{"workspace", workspace, MOE_TYPE_F32, 0, 1, (int64_t)(need / 4)};
-        if (may_overlap(rw, ro) || may_overlap(rw, rx) || (e.residual && may_overlap(rw, rr)) ||
-            (e.bias && may_overlap(rw, rb)))
-            return fail(MOE_INT4_EINVAL, "workspace overlaps out, x, residual or bias");
+        if (may_overlap(rw, ro) || may_overlap(rw, rx) || may_overlap(rw, rp) || may_overlap(rw, rs) ||
+            (e.residual && may_overlap(rw, rr)) || (e.bias && may_overlap(rw, rb)))
+            return fail(MOE_INT4_EINVAL, "workspace overlaps out, x, the weights, residual or bias");
     }
     if ((rc = check_device()) || (rc = check_stream((hipStream_t)hip_stream))) return rc;
     const Int8Epilogue d{e.bias, e.residual, out, tokens > 1 ? (size_t)x_stride : 0,

@@ -57,6 +57,8 @@ FINE = "a valid call"   # stops only where there is no gfx950 device; not made w
     (dict(out=FAKE * 2 + 1000), B.EINVAL, "out overlaps w_packed"),
     (dict(out=FAKE * 3 + 64), B.EINVAL, "out overlaps w_scales"),
     (dict(tokens=64, k=10240, xs=10240, n=96, os_=96, ws=FAKE * 4 + 64), B.EINVAL, "workspace overlaps"),
+    (dict(tokens=64, k=10240, xs=10240, n=96, os_=96, ws=FAKE * 2 + 64), B.EINVAL, "workspace overlaps"),
+    (dict(tokens=64, k=10240, xs=10240, n=96, os_=96, ws=FAKE * 3 + 64), B.EINVAL, "workspace overlaps"),
     (dict(epi=dict(activation=6)), B.EINVAL, "activation 6"),
     (dict(epi=dict(activation=-1)), B.EINVAL, "activation -1"),
     (dict(epi=dict(bias=FAKE * 5, bias_type=7)), B.EINVAL, "bias: type 7"),
