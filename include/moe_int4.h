@@ -329,7 +329,7 @@ int32_t moe_int8_linear_fused(const uint16_t *x, int64_t x_stride, const int32_t
  *   bias_ids int32, bias_values fp32 [rows][bias_width], rows bias_stride
  *            elements apart; bias_lengths int32 [rows] (NULL: every entry),
  *            clamped to [0, bias_width].  Of a token listed twice the last
- *            entry holds; a subnormal value counts as zero.
+ *            entry holds; a positive value of at most 2^-125 counts as zero.
  *   temperature  fp32 [rows] (NULL: 1); a row whose temperature is not above
  *            zero (greedy) is not scaled
  *   mask     uint32 words, rows mask_stride words apart (0: one row for all):

@@ -120,13 +120,16 @@ __global__ __launch_bounds__(NT) void logits_kernel(LogitsArgs a, int slabs, int
     // return in order): the start of the history and of the biases, whatever
     // the row's lengths, then the mask and the logits ----
     const int32_t *h = a.history + row * a.history_stride;
-    const int4 *h4 = reinterpret_cast<const int4 *>(h);
+    constexpr int kTurn = kAhead * NT;
     const int groups = vec_hist ? a.history_width / 4 : 0;   // whole groups of four
     int4 ahead[kAhead];
-    if (groups > 0) {
+    auto fetch = [&](int4 (&to)[kAhead], int g0) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) ahead[u] = h4[min(tid + u * NT, groups - 1)];
-    }
+        for (int u = 0; u < kAhead; ++u)
+            to[u] = *reinterpret_cast<const int4 *>(reinterpret_cast<const char *>(h) +
+                                                    16u * (uint32_t)min(g0 + tid + u * NT, groups - 1));
+    };
+    if (groups > 0) fetch(ahead, 0);
     const int32_t *ids = a.bias_ids + row * a.bias_stride;
     int32_t first_id = 0;
     float first_value = 0.f;
@@ -200,22 +203,10 @@ __global__ __launch_bounds__(NT) void logits_kernel(LogitsArgs a, int slabs, int
                 else atomicAdd(&s_n[at], 1u);
             }
         };
-        // kAhead groups per thread at a time; for long histories the next are
-        // on their way while these are counted
-        for (int g0 = 0; g0 < groups && 4 * g0 < hist; g0 += kAhead * NT) {
-            int4 now[kAhead];
-            const int g1 = g0 + kAhead * NT;
-            if (!LONG && g0 > 0) {
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) ahead[u] = h4[min(g0 + tid + u * NT, groups - 1)];
-            }
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) now[u] = ahead[u];
-            if (LONG && g1 < groups && 4 * g1 < hist) {
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) ahead[u] = h4[min(g1 + tid + u * NT, groups - 1)];
-            }
+        // the groups from g0 on, kAhead per thread
+        auto count = [&](const int4 (&now)[kAhead], int g0) {
             // all of it prompt, all of it behind the prompt, or something of both
+            const int g1 = g0 + kTurn;
             const bool all_prompt = 4 * g1 <= prompt, all_after = 4 * g0 >= prompt && 4 * g1 <= min(hist, 4 * groups);
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
@@ -233,6 +224,26 @@ __global__ __launch_bounds__(NT) void logits_kernel(LogitsArgs a, int slabs, int
 #pragma unroll
                     for (int e = 0; e < 4; ++e) one(4 * g + e, id[e]);
                 }
+            }
+        };
+        auto more = [&](int g0) { return g0 < groups && 4 * g0 < hist; };
+        if constexpr (LONG) {
+            // the next groups are on their way while these are counted; two
+            // buffers by name, for moving one into the other took as many
+            // vector instructions as the counting (a million ids: 56 us
+            // against 63)
+            int4 next[kAhead];
+            for (int g0 = 0; more(g0); g0 += 2 * kTurn) {
+                fetch(next, g0 + kTurn);
+                count(ahead, g0);
+                if (!more(g0 + kTurn)) break;
+                fetch(ahead, g0 + 2 * kTurn);
+                count(next, g0 + kTurn);
+            }
+        } else {
+            for (int g0 = 0; more(g0); g0 += kTurn) {
+                if (g0 > 0) fetch(ahead, g0);
+                count(ahead, g0);
             }
         }
         for (int i = 4 * groups + tid; i < hist; i += NT) one(i, h[i]);   // behind the groups
@@ -276,7 +287,7 @@ __global__ __launch_bounds__(NT) void logits_kernel(LogitsArgs a, int slabs, int
         const float *values = a.bias_values + row * a.bias_stride;
         each([&](int i, uint32_t *w) {
             if (*w != (uint32_t)i + 1u) return;
-            // a value whose bits could be taken for a place (a subnormal) is zero
+            // a value whose bits could be taken for a place (at most 2^24: 2^-125) is zero
             const uint32_t bits = __float_as_uint(i < NT ? first_value : values[i]);
             *w = bits <= (1u << 24) ? 0u : bits;
         });
@@ -343,9 +354,9 @@ void launch_in(const LogitsArgs &a, int out_type, hipStream_t st)
     // with histories of 16384, which a smaller slab scans more often.
     if ((long)a.rows * ((a.vocab + 8191) / 8192) > 512) launch_shape<512, 16, C, TIN, false>(a, out_type, st);
     // Below that, small workgroups start and end soonest (one row of 248320
-    // and a history of 512: 4.0 us against 5.4), but every workgroup scans the
+    // and a history of 512: 3.8 us against 5.4), but every workgroup scans the
     // whole history, so for wide tables it gets all the threads it can have
-    // (one row, a history of 131072: 12 us against 21).
+    // (one row, a history of 131072: 11.5 us against 21).
     else if (a.history_width > 8192) launch_shape<1024, 8, C, TIN, true>(a, out_type, st);
     else launch_shape<256, 8, C, TIN, false>(a, out_type, st);
 }

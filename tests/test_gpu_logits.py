@@ -233,6 +233,23 @@ def test_rules_long_history(rows, width):
     check(out, *expected(logits, u), f"{rows} x {width}")
 
 
+@pytest.mark.parametrize("rows,vocab,tin,tout", [(5, 30000, "fp32", "fp32"), (8, 30000, "bf16", "bf16"),
+                                                 (9, 300000, "fp32", "fp32"), (9, 300000, "fp16", "fp16")])
+def test_rules_long_history_edges(rows, vocab, tin, tout):
+    # lengths and prompts that end at, before and behind whole runs of 16384
+    # ids (1024 threads, four groups of four each), of which the scan keeps one ahead
+    say(f"long history edges {rows}x{vocab} {tin}->{tout}")
+    edges = [0, 1, 3, 16383, 16384, 16385, 32767, 32768, 32769, 49152, 49155, 65536, 65539]
+    for width in (16384, 32769, 65539):
+        logits, u = make(rows, vocab, width, 7, False, rows + width, in_type=tin)
+        rng = np.random.default_rng(width)
+        u["history_lengths"].copy_(torch.from_numpy(rng.choice(edges, rows).astype(np.int32)))
+        u["prompt_lengths"].copy_(torch.from_numpy(rng.choice(edges, rows).astype(np.int32)))
+        out = LogitsRules(vocab, **u).apply(logits, out_dtype=TYPES[tout])
+        torch.cuda.synchronize()
+        check(out, *expected(logits, u), f"{rows} x {width}")
+
+
 @pytest.mark.parametrize("tin", ["bf16", "fp16", "fp32"])
 def test_rules_special_values(tin):
     rows, vocab = 8, 4100
