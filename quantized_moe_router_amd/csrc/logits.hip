@@ -356,7 +356,11 @@ void launch_in(const LogitsArgs &a, int out_type, hipStream_t st)
     // Below that, small workgroups start and end soonest (one row of 248320
     // and a history of 512: 3.8 us against 5.4), but every workgroup scans the
     // whole history, so for wide tables it gets all the threads it can have
-    // (one row, a history of 131072: 11.5 us against 21).
+    // (one row, a history of 131072: 11.5 us against 21), with one chunk each
+    // where that takes no more workgroups than CUs (fp32: 10.7; two to a CU
+    // share its issue slots, 8 rows take 18.8 against 14.2).
+    else if (a.history_width > 8192 && (long)a.rows * ((a.vocab + 1024 * C - 1) / (1024 * C)) <= 256)
+        launch_shape<1024, C, C, TIN, true>(a, out_type, st);
     else if (a.history_width > 8192) launch_shape<1024, 8, C, TIN, true>(a, out_type, st);
     else launch_shape<256, 8, C, TIN, false>(a, out_type, st);
 }
