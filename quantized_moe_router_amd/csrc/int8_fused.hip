@@ -5,9 +5,10 @@
 //     projection);
 //   * int8_ksplit_kernel: more than four tokens and few 32 x 32 output tiles
 //     (the down projection): the waves of one workgroup split K and meet in
-//     LDS, so no partial sum goes through memory.
+//     LDS, so no partial sum goes through memory;
+//   * int8_gemv_wide_kernel: 3 or 5 to 16 tokens on wide matrices (lm_head).
 //
-// Both use v_mfma_f32_32x32x16_f16 on exact fp16 codes and activations, a
+// The first two use v_mfma_f32_32x32x16_f16 on exact fp16 codes and activations, a
 // group's sum starting from zero and folded into the accumulator with the
 // group's scale by one FMA, as int8_gemm_kernel does.  In the result a lane
 // holds one column (weight row, lane % 32) of 16 tokens: rows
@@ -38,10 +39,14 @@ struct FusedArgs {
 // and out are 8 or 16 bytes wide and a row's lanes consecutive: one or two
 // elements per lane straight from the accumulators issue four to eight times
 // the memory instructions (8192 tokens, N = 10240, K = 320, bf16 out and
-// residual: 118 us against 142 and 173).  What bounds it: with fp32 out and
-// residual the memory (680 MB in 148 us, 93 % of a copy's rate); with bf16 the
-// work per tile of three workgroups per CU (a fourth would need its registers
-// spilled), two thirds of it vector instructions.
+// residual: 114 us against 142 and 173).  Columns that share no aligned word
+// (odd N, odd strides) go element by element through the same LDS, a row's
+// lanes consecutive: 188 us for 8192 x 10239 in fp32, 59 for 4919 x 3435 with
+// GELU, where four columns per lane, an element at a time, took 411 and 91.
+// What bounds it: with fp32 out and residual the memory (680 MB in 146 us, 94 %
+// of a copy's rate); with bf16 the work per tile of three workgroups per CU (a
+// fourth would need its registers spilled), two thirds of it vector
+// instructions.
 // ---------------------------------------------------------------------------
 constexpr int kSpM = 64, kSpN = 128, kSpThreads = 256, kSpKS = 64;
 constexpr int kSpCs = kSpN + 8;   // padded row of sums (fp32 words)
@@ -61,8 +66,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const void *base, 
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), (short)0, (int)size, kBufferWord3);
 }
 
-// NS: K / 64; GS: stages per scale group; RES: bytes of a residual element (0: none).
-template <int NS, int GS, int RES>
+// NS: K / 64; GS: stages per scale group; RES: bytes of a residual element (0:
+// none); VEC: four columns lie on an aligned word in residual and out.
+template <int NS, int GS, int RES, bool VEC>
 __global__ __launch_bounds__(kSpThreads, 3) void int8_short_fused_kernel(FusedArgs g)
 {
     constexpr int LR = NS * kSpKS + 8;    // padded activation row (fp16)
@@ -111,15 +117,28 @@ __global__ __launch_bounds__(kSpThreads, 3) void int8_short_fused_kernel(FusedAr
     }
     // epilogue: this thread's four columns of rows tid / 32 + 8 u
     const int r0 = tid >> 5, c4 = 4 * (tid & 31), nn = n0 + c4;
-    const float4 bias = g.e.bias ? load_typed4(g.e.bias, g.e.bias_type, min(nn, g.N - 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (g.e.bias) {
+        if constexpr (VEC)
+            bias = load_typed4(g.e.bias, g.e.bias_type, min(nn, g.N - 4));
+        else
+            bias = make_float4(load_typed(g.e.bias, g.e.bias_type, min(nn, g.N - 1)),
+                               load_typed(g.e.bias, g.e.bias_type, min(nn + 1, g.N - 1)),
+                               load_typed(g.e.bias, g.e.bias_type, min(nn + 2, g.N - 1)),
+                               load_typed(g.e.bias, g.e.bias_type, min(nn + 3, g.N - 1)));
+    }
+    // at residual and out these columns, or, element by element, column
+    // tid % 128 of rows tid / 128 + 2 u
+    constexpr int kRowStep = VEC ? 8 : 2;
+    const int rr = VEC ? r0 : tid >> 7, rc = VEC ? c4 : tid & 127;
     auto lane_offset = [&](size_t stride, int bytes) {
-        return nn < g.N ? ((uint32_t)r0 * (uint32_t)stride + (uint32_t)nn) * (uint32_t)bytes : 0x80000000u;
+        return n0 + rc < g.N ? ((uint32_t)rr * (uint32_t)stride + (uint32_t)(n0 + rc)) * (uint32_t)bytes : 0x80000000u;
     };
     // the bias where no activation has taken it in
     const float4 late = g.e.activation == kActNone ? bias : make_float4(0.f, 0.f, 0.f, 0.f);
     const int ob = type_bytes(g.e.out_type);
-    const uint32_t roff = lane_offset(g.e.residual_stride, RES), rstep = 8u * (uint32_t)g.e.residual_stride * RES;
-    const uint32_t ooff = lane_offset(g.e.out_stride, ob), ostep = 8u * (uint32_t)g.e.out_stride * ob;
+    const uint32_t roff = lane_offset(g.e.residual_stride, RES), rstep = kRowStep * (uint32_t)g.e.residual_stride * RES;
+    const uint32_t ooff = lane_offset(g.e.out_stride, ob), ostep = kRowStep * (uint32_t)g.e.out_stride * ob;
 
     for (int mi = tile / g.ntiles; mi < g.mtiles; mi += g.mstep) {
     const int m0 = mi * kSpM, rows = min(kSpM, g.T - m0);
@@ -174,24 +193,31 @@ __global__ __launch_bounds__(kSpThreads, 3) void int8_short_fused_kernel(FusedAr
     }
 
     // ---- epilogue ----
-    u32x4_t res[8];
-    if constexpr (RES > 0) {
+    constexpr int kPer = 32 / kRowStep;   // accesses per thread to 32 rows
+    u32x4_t res[VEC ? 2 * kPer : 1];
+    uint32_t res1[VEC ? 1 : 2 * kPer];
+    auto load_residual = [&](int h) {
+        const __amdgpu_buffer_rsrc_t rs = rows_buffer<32>(g.e.residual, g.e.residual_stride, RES, m0 + 32 * h, g.T, g.N);
+        uint32_t off = roff;
+        if constexpr (!VEC) asm volatile("" : "+v"(off));   // 16 offsets made here, not kept over the tiles
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const __amdgpu_buffer_rsrc_t rs =
-                rows_buffer<32>(g.e.residual, g.e.residual_stride, RES, m0 + 32 * h, g.T, g.N);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int at = (int)(roff + u * rstep);
-                if constexpr (RES == 4) {
-                    res[4 * h + u] = __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, 0);
-                } else {
-                    const u32x2_t w = __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, 0);
-                    res[4 * h + u][0] = w[0];
-                    res[4 * h + u][1] = w[1];
-                }
+        for (int u = 0; u < kPer; ++u) {
+            const int at = (int)(off + u * rstep);
+            if constexpr (!VEC) {
+                if constexpr (RES == 4) res1[kPer * h + u] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0);
+                else res1[kPer * h + u] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, at, 0, 0);
+            } else if constexpr (RES == 4) {
+                res[kPer * h + u] = __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, 0);
+            } else {
+                const u32x2_t w = __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, 0);
+                res[kPer * h + u][0] = w[0];
+                res[kPer * h + u][1] = w[1];
             }
         }
+    };
+    if constexpr (RES > 0) {
+        load_residual(0);
+        if constexpr (VEC) load_residual(1);
     }
     __syncthreads();   // the activations have been read
 #pragma unroll
@@ -200,9 +226,10 @@ __global__ __launch_bounds__(kSpThreads, 3) void int8_short_fused_kernel(FusedAr
         for (int j = 0; j < 16; ++j)
             s_c[(32 * mt + 8 * (j >> 2) + 4 * half + (j & 3)) * kSpCs + 32 * wave + (lane & 31)] = acc[mt][j];
     __syncthreads();
+    if constexpr (RES > 0 && !VEC) load_residual(1);   // the accumulators' registers are free
     // an activation in place (this thread's own words), in a loop of its own:
     // unrolled with the stores it was 25 KB of code, fetched at every launch
-    if (g.e.activation != kActNone) {
+    if (g.e.activation != kActNone || (!VEC && g.e.bias)) {
 #pragma unroll 1
         for (int u = 0; u < kSpM / 8; ++u) {
             float4 *w = reinterpret_cast<float4 *>(s_c + (8 * u + r0) * kSpCs + c4);
@@ -211,15 +238,34 @@ __global__ __launch_bounds__(kSpThreads, 3) void int8_short_fused_kernel(FusedAr
                              activate(f.z + bias.z, g.e.activation), activate(f.w + bias.w, g.e.activation));
         }
     }
+    if constexpr (!VEC) __syncthreads();   // the words of other threads
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         if (32 * h >= rows) break;
         const __amdgpu_buffer_rsrc_t rs = rows_buffer<32>(g.e.out, g.e.out_stride, ob, m0 + 32 * h, g.T, g.N);
+        uint32_t off = ooff;
+        if constexpr (!VEC) asm volatile("" : "+v"(off));
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kPer; ++u) {
+            const int at = (int)(off + u * ostep);
+            if constexpr (!VEC) {
+                float v = s_c[(32 * h + kRowStep * u + rr) * kSpCs + rc];
+                if constexpr (RES > 0) {
+                    const uint32_t w = res1[kPer * h + u];
+                    v += RES == 4                       ? __uint_as_float(w)
+                         : g.e.residual_type == kBf16 ? bf16_lo(w)
+                                                        : (float)__builtin_bit_cast(f16x2_t, w)[0];
+                }
+                if (g.e.out_type == kF32)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rs, at, 0, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b16(
+                        g.e.out_type == kBf16 ? (uint16_t)f32_to_bf16(v) : __builtin_bit_cast(uint16_t, (_Float16)v), rs, at, 0, 0);
+                continue;
+            }
             const float4 f = *reinterpret_cast<const float4 *>(s_c + (32 * h + 8 * u + r0) * kSpCs + c4);
             float v[4] = {f.x + late.x, f.y + late.y, f.z + late.z, f.w + late.w};
-            const u32x4_t w = res[4 * h + u];
+            const u32x4_t w = res[VEC ? kPer * h + u : 0];
             if constexpr (RES == 4) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -236,7 +282,6 @@ __global__ __launch_bounds__(kSpThreads, 3) void int8_short_fused_kernel(FusedAr
                     v[2 * q + 1] += bf ? bf16_hi(e) : (float)hh[1];
                 }
             }
-            const int at = (int)(ooff + u * ostep);
             if (g.e.out_type == kF32) {
                 const u32x4_t o = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
                 __builtin_amdgcn_raw_buffer_store_b128(o, rs, at, 0, 0);
@@ -578,21 +623,21 @@ __global__ __launch_bounds__(kGwThreads, 4) void int8_gemv_wide_kernel(FusedArgs
     }
 }
 
-template <int RES>
+template <int RES, bool VEC>
 void launch_short(const FusedArgs &a, int grid, hipStream_t st)
 {
     const int ns = a.K / kSpKS;
     if (a.gshift == 6) {
         switch (ns) {
-        case 1: int8_short_fused_kernel<1, 1, RES><<<grid, kSpThreads, 0, st>>>(a); break;
-        case 2: int8_short_fused_kernel<2, 1, RES><<<grid, kSpThreads, 0, st>>>(a); break;
-        case 3: int8_short_fused_kernel<3, 1, RES><<<grid, kSpThreads, 0, st>>>(a); break;
-        case 4: int8_short_fused_kernel<4, 1, RES><<<grid, kSpThreads, 0, st>>>(a); break;
-        default: int8_short_fused_kernel<5, 1, RES><<<grid, kSpThreads, 0, st>>>(a); break;
+        case 1: int8_short_fused_kernel<1, 1, RES, VEC><<<grid, kSpThreads, 0, st>>>(a); break;
+        case 2: int8_short_fused_kernel<2, 1, RES, VEC><<<grid, kSpThreads, 0, st>>>(a); break;
+        case 3: int8_short_fused_kernel<3, 1, RES, VEC><<<grid, kSpThreads, 0, st>>>(a); break;
+        case 4: int8_short_fused_kernel<4, 1, RES, VEC><<<grid, kSpThreads, 0, st>>>(a); break;
+        default: int8_short_fused_kernel<5, 1, RES, VEC><<<grid, kSpThreads, 0, st>>>(a); break;
         }
     } else {
-        if (ns == 2) int8_short_fused_kernel<2, 2, RES><<<grid, kSpThreads, 0, st>>>(a);
-        else int8_short_fused_kernel<4, 2, RES><<<grid, kSpThreads, 0, st>>>(a);
+        if (ns == 2) int8_short_fused_kernel<2, 2, RES, VEC><<<grid, kSpThreads, 0, st>>>(a);
+        else int8_short_fused_kernel<4, 2, RES, VEC><<<grid, kSpThreads, 0, st>>>(a);
     }
 }
 
@@ -614,9 +659,10 @@ hipError_t launch_int8_short_fused(const uint16_t *x, const int32_t *wq, const u
     const int most = kSlots / a.ntiles > 0 ? kSlots / a.ntiles : 1, turns = (a.mtiles + most - 1) / most;
     a.mstep = (a.mtiles + turns - 1) / turns;
     const int grid = (a.mstep * a.ntiles + 7) / 8 * 8;
-    if (!e.residual) launch_short<0>(a, grid, st);
-    else if (e.residual_type == kF32) launch_short<4>(a, grid, st);
-    else launch_short<2>(a, grid, st);
+    const int res = !e.residual ? 0 : type_bytes(e.residual_type);
+    if (res == 0) e.vec ? launch_short<0, true>(a, grid, st) : launch_short<0, false>(a, grid, st);
+    else if (res == 4) e.vec ? launch_short<4, true>(a, grid, st) : launch_short<4, false>(a, grid, st);
+    else e.vec ? launch_short<2, true>(a, grid, st) : launch_short<2, false>(a, grid, st);
     return hipGetLastError();
 }
 

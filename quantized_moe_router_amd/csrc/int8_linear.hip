@@ -750,10 +750,9 @@ constexpr size_t go_lds_bytes()
     return x > c ? x : c;
 }
 
-template <int NS, int GS, bool F>
+template <int NS, int GS>
 __global__ __launch_bounds__(kGoThreads, 1) void int8_gemm_short_kernel(Int8GemmArgs g)
 {
-    const size_t xstride = F ? g.e.x_stride : (size_t)g.K;
     constexpr int LR = NS * kGmKS + 8;    // padded activation row (fp16)
     constexpr int CH = NS * 8;            // 16-byte chunks per activation row
     constexpr int XPER = (kGmM * CH + kGoThreads - 1) / kGoThreads;
@@ -788,7 +787,7 @@ __global__ __launch_bounds__(kGoThreads, 1) void int8_gemm_short_kernel(Int8Gemm
 #pragma unroll
     for (int u = 0; u < XPER; ++u) {
         const int c = min(tid + kGoThreads * u, kGmM * CH - 1), r = c / CH, col = c % CH;
-        rx[u] = *reinterpret_cast<const u32x4_t *>(g.x + (m0 + (r < rows ? r : 0)) * xstride + 8 * col);
+        rx[u] = *reinterpret_cast<const u32x4_t *>(g.x + (size_t)(m0 + (r < rows ? r : 0)) * g.K + 8 * col);
     }
     const int gpr = g.K >> g.gshift;   // groups per weight row
     uint32_t rsc[SPER];
@@ -861,7 +860,7 @@ __global__ __launch_bounds__(kGoThreads, 1) void int8_gemm_short_kernel(Int8Gemm
     // ---- epilogue through LDS, 64 tokens at a time (as in int8_gemm_kernel) ----
     __syncthreads();   // every wave is done reading the activations
     float *s_c = reinterpret_cast<float *>(s_raw);
-    const bool vec = F ? g.e.vec : (g.N & 3) == 0;
+    const bool vec = (g.N & 3) == 0;
 #pragma unroll
     for (int hp = 0; hp < 2; ++hp) {
         if (64 * hp >= rows) break;   // uniform over the workgroup
@@ -874,7 +873,6 @@ __global__ __launch_bounds__(kGoThreads, 1) void int8_gemm_short_kernel(Int8Gemm
                     acc[2 * hp + u][j];
         }
         __syncthreads();
-#pragma unroll 1
         for (int it = tid; it < 64 * (kGoN / 4); it += kGoThreads) {
             const int r = it / (kGoN / 4), c4 = 4 * (it % (kGoN / 4));
             const int m = 64 * hp + r, nn = n0 + c4;
@@ -882,18 +880,14 @@ __global__ __launch_bounds__(kGoThreads, 1) void int8_gemm_short_kernel(Int8Gemm
             const float4 v = *reinterpret_cast<const float4 *>(s_c + r * kGoCs + c4);
             const size_t o = (size_t)(m0 + m) * g.N + nn;
             if (vec) {
-                if constexpr (F)
-                    finish4(g.e, m0 + m, nn, v);
-                else
-                    *reinterpret_cast<uint2 *>(g.out + o) =
-                        make_uint2(f32x2_to_bf16x2(v.x, v.y), f32x2_to_bf16x2(v.z, v.w));
+                *reinterpret_cast<uint2 *>(g.out + o) =
+                    make_uint2(f32x2_to_bf16x2(v.x, v.y), f32x2_to_bf16x2(v.z, v.w));
             } else {
                 const float e4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if (nn + e >= g.N) break;
-                    if constexpr (F) finish(g.e, m0 + m, nn + e, e4[e]);
-                    else g.out[o + e] = (uint16_t)f32_to_bf16(e4[e]);
+                    g.out[o + e] = (uint16_t)f32_to_bf16(e4[e]);
                 }
             }
         }
@@ -1090,19 +1084,19 @@ hipError_t launch_plan(const Int8Plan &p, const uint16_t *x, const int32_t *wq, 
     a.e = e;
     const long tiles = (long)p.mtiles * p.ntiles * p.ksplit;
     const int grid = (int)((tiles + 7) / 8 * 8);
-    if (p.short_k) {
+    if constexpr (!F) if (p.short_k) {   // the fused layer has a kernel of its own
         const int ns = K / kGmKS;
         if (G == 64) {
             switch (ns) {
-            case 1: int8_gemm_short_kernel<1, 1, F><<<grid, kGoThreads, 0, st>>>(a); break;
-            case 2: int8_gemm_short_kernel<2, 1, F><<<grid, kGoThreads, 0, st>>>(a); break;
-            case 3: int8_gemm_short_kernel<3, 1, F><<<grid, kGoThreads, 0, st>>>(a); break;
-            case 4: int8_gemm_short_kernel<4, 1, F><<<grid, kGoThreads, 0, st>>>(a); break;
-            default: int8_gemm_short_kernel<5, 1, F><<<grid, kGoThreads, 0, st>>>(a); break;
+            case 1: int8_gemm_short_kernel<1, 1><<<grid, kGoThreads, 0, st>>>(a); break;
+            case 2: int8_gemm_short_kernel<2, 1><<<grid, kGoThreads, 0, st>>>(a); break;
+            case 3: int8_gemm_short_kernel<3, 1><<<grid, kGoThreads, 0, st>>>(a); break;
+            case 4: int8_gemm_short_kernel<4, 1><<<grid, kGoThreads, 0, st>>>(a); break;
+            default: int8_gemm_short_kernel<5, 1><<<grid, kGoThreads, 0, st>>>(a); break;
             }
         } else {
-            if (ns == 2) int8_gemm_short_kernel<2, 2, F><<<grid, kGoThreads, 0, st>>>(a);
-            else int8_gemm_short_kernel<4, 2, F><<<grid, kGoThreads, 0, st>>>(a);
+            if (ns == 2) int8_gemm_short_kernel<2, 2><<<grid, kGoThreads, 0, st>>>(a);
+            else int8_gemm_short_kernel<4, 2><<<grid, kGoThreads, 0, st>>>(a);
         }
         return hipGetLastError();
     }
@@ -1165,7 +1159,7 @@ hipError_t launch_int8_linear_fused(const uint16_t *x, const int32_t *wq, const 
 {
     const Int8Plan p = int8_fused_plan(T, N, K, G);
     if (p.wide) return launch_int8_gemv_wide(x, wq, ws, T, N, K, G, e, st);
-    if (p.short_k && e.vec) return launch_int8_short_fused(x, wq, ws, T, N, K, G, e, st);
+    if (p.short_k) return launch_int8_short_fused(x, wq, ws, T, N, K, G, e, st);
     if (p.kwaves) {
         float *part = static_cast<float *>(workspace);
         const hipError_t rc = launch_int8_ksplit(x, wq, ws, T, N, K, G, e, p.ksplit, part, p.pstride, st);

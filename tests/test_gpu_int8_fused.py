@@ -215,6 +215,23 @@ def test_fused_small(T, N, K, G, bias, kind, residual, out, strided):
         assert bool((d["wide"]["out"][:, N:] == 55.0).all())
 
 
+@pytest.mark.parametrize("T,N,K,G,bias,kind,residual,out", [
+    (5000, 1283, 64, 64, "bf16", "silu", "fp32", "fp16"), (3000, 2051, 320, 64, None, "none", "bf16", "fp32"),
+    (4500, 1025, 256, 128, "fp32", "gelu", "fp16", "bf16"), (4900, 1154, 192, 64, "fp16", "none", None, "fp32"),
+    (2500, 1283, 128, 128, None, "sigmoid", "fp32", "fp32"), (1100, 711, 384, 64, "bf16", "gelu", "fp32", "fp32"),
+    (2100, 1283, 640, 128, "fp32", "silu", "bf16", "fp16"), (2000, 1030, 448, 64, None, "none", "fp16", "bf16")])
+@pytest.mark.parametrize("strided", [False, True])
+def test_fused_many_tokens_of_unaligned_rows(T, N, K, G, bias, kind, residual, out, strided):
+    # several token tiles to a workgroup, columns that share no aligned word
+    label = f"unaligned T={T} N={N} K={K} {kind} {residual}->{out} {strided}"
+    say(label)
+    layer, d = case(T, N, K, G, bias, residual, out, strided, seed=T)
+    got = run(d, kind)
+    torch.cuda.synchronize()
+    want, err = expected(layer, d, kind)
+    check(got, want, err, TYPES[out], label)
+
+
 @pytest.mark.parametrize("which,T", [("down", 512), ("up", 512), ("up", 2000)])
 def test_fused_mixer_shapes(which, T):
     N, K = (320, 10240) if which == "down" else (10240, 320)
