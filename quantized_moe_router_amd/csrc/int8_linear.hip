@@ -1132,7 +1132,11 @@ hipError_t launch_int8_linear(const uint16_t *x, const int32_t *wq, const uint16
 // tokens 6.3, 12.4; 512 tokens, 512 tiles, 12.7, 19.5).  A K of many stages
 // per wave is split over workgroups too where the tiles leave most CUs idle:
 // 32 tokens of N = 320, K = 10240 take 17.9 us unsplit, 8.1 in 16 parts; from
-// K = 5120 that pays for the second launch.
+// K = 5120 that pays for the second launch.  Of the short K's, those of three
+// groups or more that take it: 150 x 1295 x 320 with GELU 7.8 us against 15.4,
+// 64 x 1280 x 192 with SiLU 8.0 against 10.0; of 320 tiles on int8_short_fused_kernel
+// is faster (17 x 10240 x 192 8.1 us against 9.2), and for one or two groups,
+// where a workgroup has as few waves (64 x 1280 x 64 9.3 against 12.0).
 Int8Plan int8_fused_plan(int T, int N, int K, int G)
 {
     Int8Plan p = int8_plan(T, N, K, G);
@@ -1142,9 +1146,10 @@ Int8Plan int8_fused_plan(int T, int N, int K, int G)
         p = Int8Plan{};
         p.gemv = p.wide = true;
     }
-    if (p.gemv || T == 0 || p.short_k) return p;
+    if (p.gemv || T == 0) return p;
     const long tiles = (long)((T + 31) / 32) * ((N + 31) / 32);
-    if (tiles > (K <= 2560 ? 512 : 256)) return p;
+    if (tiles > (K > 320 && K <= 2560 ? 512 : 256) || (p.short_k && K < 3 * G)) return p;
+    p.short_k = false;
     p.kwaves = true;
     int ks = K >= 5120 ? (int)(192 / tiles) : 1;
     ks = ks < kInt8MaxSplitK ? ks : kInt8MaxSplitK;
