@@ -99,4 +99,33 @@ __device__ __forceinline__ void finish4(const Int8Epilogue &e, int t, int r, flo
     store_typed4(e.out, e.out_type, t * e.out_stride + r, v);
 }
 
+// Column r of rows t, t + step, .. (four, those below T), with its bias: for
+// outputs whose columns share no aligned word.  The residual is asked for
+// first, so that its four loads are waited for once.
+__device__ __forceinline__ void finish_rows(const Int8Epilogue &e, int t, int step, int T, int r, float bias,
+                                            const float (&v)[4])
+{
+    float res[4] = {0.f, 0.f, 0.f, 0.f};
+    if (e.residual) {
+        size_t at[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[i] = min(t + i * step, T - 1) * e.residual_stride + r;
+        if (e.residual_type == kF32) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) res[i] = static_cast<const float *>(e.residual)[at[i]];
+        } else {
+            uint16_t b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = static_cast<const uint16_t *>(e.residual)[at[i]];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                res[i] = e.residual_type == kBf16 ? bf16_to_f32(b[i]) : (float)__builtin_bit_cast(_Float16, b[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (t + i * step < T)
+            store_typed(e.out, e.out_type, (t + i * step) * e.out_stride + r, activate(v[i] + bias, e.activation) + res[i]);
+}
+
 }  // namespace moe
