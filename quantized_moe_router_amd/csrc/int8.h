@@ -128,4 +128,33 @@ __device__ __forceinline__ void finish_rows(const Int8Epilogue &e, int t, int st
             store_typed(e.out, e.out_type, (t + i * step) * e.out_stride + r, activate(v[i] + bias, e.activation) + res[i]);
 }
 
+// Columns r .. r + 3 of rows t, t + step, .. (four, those below T), bias and
+// activation taken in already, r a multiple of 4 and e.vec set: the residual's
+// four loads are waited for once.
+__device__ __forceinline__ void finish_rows4(const Int8Epilogue &e, int t, int step, int T, int r, float4 (&v)[4])
+{
+    if (e.residual) {
+        float4 res[4];
+        if (e.residual_type == kF32) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                res[i] = load_typed4(e.residual, kF32, min(t + i * step, T - 1) * e.residual_stride + r);
+        } else if (e.residual_type == kBf16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                res[i] = load_typed4(e.residual, kBf16, min(t + i * step, T - 1) * e.residual_stride + r);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                res[i] = load_typed4(e.residual, kF16, min(t + i * step, T - 1) * e.residual_stride + r);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = make_float4(v[i].x + res[i].x, v[i].y + res[i].y, v[i].z + res[i].z, v[i].w + res[i].w);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (t + i * step < T) store_typed4(e.out, e.out_type, (t + i * step) * e.out_stride + r, v[i]);
+}
+
 }  // namespace moe
