@@ -297,6 +297,19 @@ def moe_int8_linear_fused_workspace_bytes(tokens: int, n: int, k: int, group: in
     return b.value
 
 
+def check_int8_weights(w_packed, w_scales, n: int, k: int, group: int):
+    """The codes and scales of an [n, k] INT8 weight: the library reads that
+    many of them from their addresses on."""
+    import torch
+    if w_packed.dtype != torch.int32 or w_packed.shape != (n, k // 4) or not w_packed.is_contiguous():
+        raise ValueError(f"w_packed is {w_packed.dtype} {tuple(w_packed.shape)}, expected contiguous int32 "
+                         f"({n}, {k} / 4)")
+    if group <= 0 or type_code(w_scales.dtype) != TYPE_BF16 or w_scales.shape != (n, k // group) \
+            or not w_scales.is_contiguous():
+        raise ValueError(f"w_scales is {w_scales.dtype} {tuple(w_scales.shape)}, expected contiguous bfloat16 "
+                         f"({n}, {k} / {group})")
+
+
 def moe_int8_linear_fused(x, w_packed, w_scales, tokens: int, n: int, k: int, group: int, out,
                           bias=None, residual=None, activation: str = "none", workspace=None, stream=None):
     """out [tokens, n] = residual + act(x W^T + bias): x bf16 [tokens, k],
@@ -304,6 +317,14 @@ def moe_int8_linear_fused(x, w_packed, w_scales, tokens: int, n: int, k: int, gr
     [tokens, n]; bias, residual and out in bf16, fp16 or fp32, the rows of x,
     residual and out possibly inside wider ones.  activation: a key of
     ACTIVATIONS.  workspace: uint8, may be None when the shape needs none."""
+    check_int8_weights(w_packed, w_scales, n, k, group)
+    int8_linear_fused(x, w_packed, w_scales, tokens, n, k, group, out, bias, residual, activation, workspace, stream)
+
+
+def int8_linear_fused(x, w_packed, w_scales, tokens: int, n: int, k: int, group: int, out, bias, residual,
+                      activation: str, workspace, stream=None):
+    """moe_int8_linear_fused on weights that have passed check_int8_weights
+    (layer.Int8Linear checks its own once)."""
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation {activation!r} is none of {', '.join(ACTIVATIONS)}")
@@ -319,18 +340,20 @@ def moe_int8_linear_fused(x, w_packed, w_scales, tokens: int, n: int, k: int, gr
     if residual is not None:
         e.residual_stride = row_stride(residual, "residual", tokens, n)
         e.residual, e.residual_type = residual.data_ptr(), type_code(residual.dtype)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError(f"workspace is {tuple(workspace.shape)} with strides {workspace.stride()}, expected contiguous")
     index = device_index(x, "x")
     if index != _current_device():   # its stream, and its device for the launch
         with _device(index):
-            return moe_int8_linear_fused(x, w_packed, w_scales, tokens, n, k, group, out, bias, residual, activation,
-                                         workspace, stream)
+            return int8_linear_fused(x, w_packed, w_scales, tokens, n, k, group, out, bias, residual, activation,
+                                     workspace, stream)
     for name, t in (("w_packed", w_packed), ("w_scales", w_scales), ("out", out), ("bias", bias),
                     ("residual", residual), ("workspace", workspace)):
         if t is not None:
             device_index(t, name, index)
     rc = lib().moe_int8_linear_fused(x.data_ptr(), x_stride, w_packed.data_ptr(), w_scales.data_ptr(), tokens, n, k,
                                      group, ctypes.byref(e), out.data_ptr(), out_type, out_stride,
-                                     _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                     _ptr(workspace), 0 if workspace is None else workspace.nbytes,
                                      _stream_on(stream, index))
     if rc:
         _check(rc)

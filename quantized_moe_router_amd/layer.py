@@ -104,8 +104,8 @@ class Int8Linear:
         # taken anew for every call: the allocator orders it by stream, and
         # two calls in flight never share one
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-        B.moe_int8_linear_fused(x, self.packed, self.scales, tokens, self.n, self.k, self.group, out, self.bias,
-                                residual, self.activation, workspace)
+        B.int8_linear_fused(x, self.packed, self.scales, tokens, self.n, self.k, self.group, out, self.bias, residual,
+                            self.activation, workspace)
         return out
 
 

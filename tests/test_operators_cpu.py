@@ -184,6 +184,29 @@ def test_int8_linear_class_checks():
         lin.forward(x)
 
 
+@pytest.mark.parametrize("bad,msg", [
+    (dict(w_packed=torch.zeros(16, 31, dtype=torch.int32)), "w_packed is"),          # too few words a row
+    (dict(w_packed=torch.zeros(15, 32, dtype=torch.int32)), "w_packed is"),          # too few rows
+    (dict(w_packed=torch.zeros(32, 16, dtype=torch.int32).t()), "w_packed is"),      # transposed
+    (dict(w_packed=torch.zeros(16, 64, dtype=torch.int32)[:, :32]), "w_packed is"),  # inside wider rows
+    (dict(w_packed=torch.zeros(16, 32, dtype=torch.int8)), "w_packed is"),           # a quarter of the bytes
+    (dict(w_scales=torch.zeros(16, 1, dtype=torch.bfloat16)), "w_scales is"),        # of groups of 128
+    (dict(w_scales=torch.zeros(16, 2)), "w_scales is"),
+    (dict(w_scales=torch.zeros(16, 2, dtype=torch.float16)), "w_scales is"),
+    (dict(w_scales=torch.zeros(2, 16, dtype=torch.bfloat16).t()), "w_scales is"),
+    (dict(group=0), "w_scales is"),
+    (dict(workspace=torch.zeros(1, dtype=torch.uint8).expand(1 << 20)), "workspace is"),
+])
+def test_fused_call_checks_what_it_dereferences(bad, msg):
+    fine = dict(x=torch.zeros(3, 128, dtype=torch.bfloat16), w_packed=torch.zeros(16, 32, dtype=torch.int32),
+                w_scales=torch.zeros(16, 2, dtype=torch.bfloat16), tokens=3, n=16, k=128, group=64,
+                out=torch.zeros(3, 16))
+    with pytest.raises(ValueError, match="x must be on the GPU"):
+        B.moe_int8_linear_fused(**fine)
+    with pytest.raises(ValueError, match=msg):
+        B.moe_int8_linear_fused(**{**fine, **bad})
+
+
 def test_logits_rules_class_checks():
     i, f = torch.int32, torch.float32
     ok = dict(history=torch.zeros(3, 5, dtype=i), repetition=torch.ones(3))
