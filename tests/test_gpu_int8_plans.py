@@ -1,0 +1,138 @@
+"""moe_int8_linear_fused kernel by kernel: shapes that provably run each of
+them (the plan is asked of the built library) where a shape chosen by size
+alone might come to another, and what only some shapes of a kernel reach.
+
+Tolerances as in test_gpu_int8_fused.py."""
+import ctypes
+import math
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from quantized_moe_router_amd import _binding as B
+from test_gpu_int8_fused import TYPES, case, check, expected, inside, run
+
+gpu = pytest.mark.gpu
+
+
+def say(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+class Plan(ctypes.Structure):
+    """Int8Plan of csrc/common.h."""
+    _fields_ = ([(f, ctypes.c_bool) for f in ("gemv", "rowsplit", "mfma", "short_k")]
+                + [(f, ctypes.c_int) for f in ("mtiles", "ntiles", "ksplit", "kslice")]
+                + [(f, ctypes.c_size_t) for f in ("pstride", "part_bytes")]
+                + [(f, ctypes.c_bool) for f in ("wide", "kwaves")])
+
+
+def plan(T, N, K, G):
+    f = B.lib()._ZN3moe15int8_fused_planEiiii
+    f.restype, f.argtypes = Plan, [ctypes.c_int] * 4
+    return f(T, N, K, G)
+
+
+def kernel(T, N, K, G):
+    p = plan(T, N, K, G)
+    if p.wide:
+        return "wide"
+    if p.gemv:
+        return "rowsplit" if p.rowsplit else "mfma" if p.mfma else "gemv"
+    if p.short_k:
+        return "short"
+    return ("kwaves" if p.kwaves else "gemm") + (" split" if p.ksplit > 1 else "")
+
+
+# ---------------------------------------------------------------------------
+# The GEMM of many tiles, rows with aligned words: ragged last tiles of one to
+# four runs of 32 tokens, columns of a last tile that is not full, every
+# activation, each type in each place, more scale groups than are staged at a
+# time, and K over workgroups.
+# ---------------------------------------------------------------------------
+GEMM = [
+    # (T, N, K, G, bias, activation, residual, out, strided)
+    (1100, 1280, 384, 64, "bf16", "silu", "fp32", "fp32", False),
+    (1030, 1284, 384, 128, "fp32", "gelu", "fp16", "bf16", False),
+    (1024, 1152, 384, 64, None, "none", "bf16", "bf16", True),
+    (1061, 1156, 384, 128, "fp16", "gelu_tanh", None, "fp16", True),
+    (1217, 1408, 384, 64, None, "sigmoid", "fp32", "fp16", False),
+    (1249, 1028, 384, 128, "bf16", "relu", "bf16", "fp32", True),
+    (2100, 2048, 640, 128, None, "none", None, "fp32", False),
+    (2050, 2052, 512, 64, "fp32", "none", "fp32", "fp32", True),
+    (2100, 2048, 4224, 64, "bf16", "silu", "bf16", "fp32", False),
+]
+SPLIT = [
+    (1024, 320, 10240, 64, "bf16", "silu", None, "bf16", False),
+    (1024, 320, 10240, 64, None, "none", "fp32", "fp32", True),
+    (900, 324, 10240, 128, "fp32", "gelu", "fp16", "fp16", False),
+    (600, 968, 2688, 64, "fp16", "sigmoid", "bf16", "fp32", True),
+    (1500, 1280, 1280, 128, None, "gelu_tanh", "fp32", "bf16", False),
+]
+
+
+@pytest.mark.parametrize("shape", sorted({c[:4] for c in GEMM + SPLIT}))
+def test_the_shapes_run_the_kernels_they_are_here_for(shape):
+    T, N, K, G = shape
+    assert kernel(*shape) == ("gemm" if any(c[:4] == shape for c in GEMM) else "gemm split")
+    assert N % 4 == 0
+    if shape == (2100, 2048, 4224, 64):
+        assert K // G > 64
+
+
+def aligned_rows(d, T, N):
+    """x, residual and out inside wider rows that keep four columns on a word."""
+    wide_x, d["x"] = inside(d["x"], 24, math.nan)
+    wide, d["out"] = inside(d["out"], 12, 55.0)
+    if d["residual"] is not None:
+        _, d["residual"] = inside(d["residual"], 8, math.nan)
+    return wide
+
+
+@gpu
+@pytest.mark.parametrize("T,N,K,G,bias,kind,residual,out,strided", GEMM + SPLIT)
+def test_gemm_aligned_rows(T, N, K, G, bias, kind, residual, out, strided):
+    label = f"{kernel(T, N, K, G)} T={T} N={N} K={K} G={G} {bias} {kind} {residual}->{out} {strided}"
+    say(label)
+    layer, d = case(T, N, K, G, bias, residual, out, False, seed=T + N)
+    wide = aligned_rows(d, T, N) if strided else None
+    got = run(d, kind)
+    torch.cuda.synchronize()
+    # the first, the last and both sides of the tiles' and passes' edges
+    toks = np.unique(np.concatenate([[0, 31, 32, 63, 64, 127, 128, T - 2, T - 1, T // 128 * 128 - 1, T // 128 * 128],
+                                     np.random.default_rng(T).choice(T, 24, replace=False)]).clip(0, T - 1))
+    want, err = expected(layer, d, kind, toks)
+    check(got[torch.from_numpy(toks).cuda()], want, err, TYPES[out], label)
+    assert bool(torch.isfinite(got).all()) and not bool((got == 77.0).all(1).any())
+    if strided:
+        assert bool((wide[:, N:] == 55.0).all())
+
+
+@gpu
+@pytest.mark.parametrize("T,N,K,G", [(1100, 1280, 384, 64), (1030, 1284, 384, 128), (1024, 320, 10240, 64),
+                                     (8, 66001, 2560, 128), (100, 1284, 320, 64), (2100, 1284, 320, 64)])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_residual_in_place(T, N, K, G, out):
+    label = f"in place, {kernel(T, N, K, G)} T={T} N={N} K={K} {out}"
+    say(label)
+    layer, d = case(T, N, K, G, "bf16", out, out, False, seed=T + 2 * N)
+    rows = np.unique(np.random.default_rng(N).choice(N, min(N, 1200), replace=False))
+    toks = np.unique(np.random.default_rng(T).choice(T, min(T, 30), replace=False))
+    sub, ds = pick_rows(layer, d, rows)
+    want, err = expected(sub, ds, "silu", toks)
+    d["out"] = d["residual"]
+    got = run(d, "silu")
+    torch.cuda.synchronize()
+    check(got[torch.from_numpy(toks).cuda()][:, torch.from_numpy(rows).cuda()], want, err, TYPES[out], label)
+
+
+def pick_rows(layer, d, rows):
+    """The layer and its data of some weight rows alone."""
+    at = torch.from_numpy(rows).cuda()
+    sub = {**layer, "packed": np.ascontiguousarray(layer["packed"][rows]),
+           "scales": np.ascontiguousarray(layer["scales"][rows])}
+    ds = {**d, "bias": None if d["bias"] is None else d["bias"][at],
+          "residual": None if d["residual"] is None else d["residual"][:, at].clone()}
+    return sub, ds
