@@ -15,6 +15,7 @@ from quantized_moe_router_amd import _binding as B
 from test_gpu_int8_fused import TYPES, case, check, expected, inside, run
 
 gpu = pytest.mark.gpu
+CUS = 256
 
 
 def say(*a):
@@ -46,6 +47,13 @@ def kernel(T, N, K, G):
     return ("kwaves" if p.kwaves else "gemm") + (" split" if p.ksplit > 1 else "")
 
 
+def wide_blocks(T, N, K):
+    """Row blocks of the wave that has most (two workgroups of eight waves to a
+    CU, one where the activations take most of its LDS)."""
+    most = (2 if T * (K // 8 + 1) * 16 <= 57344 else 1) * CUS * 8
+    return -(-(-(-N // 16)) // most)
+
+
 # ---------------------------------------------------------------------------
 # The GEMM of many tiles, rows with aligned words: ragged last tiles of one to
 # four runs of 32 tokens, columns of a last tile that is not full, every
@@ -71,13 +79,29 @@ SPLIT = [
     (600, 968, 2688, 64, "fp16", "sigmoid", "bf16", "fp32", True),
     (1500, 1280, 1280, 128, None, "gelu_tanh", "fp32", "bf16", False),
 ]
+# more blocks than waves; the steps of 128 inputs no multiple of the four that
+# are on their way; a second, partial chunk of 16 scale groups
+WIDE = [
+    (5, 70003, 640, 64, "bf16", "silu", "bf16", "fp32"),
+    (8, 66001, 2560, 128, None, "none", None, "fp32"),
+    (16, 70001, 640, 128, "fp32", "none", "fp32", "bf16"),
+    (16, 66003, 2688, 64, None, "gelu", None, "fp32"),
+    (5, 140001, 1408, 64, "fp16", "none", "fp16", "fp16"),
+    (3, 66004, 1152, 128, None, "sigmoid", None, "fp32"),
+    (12, 35001, 4224, 64, "bf16", "none", "bf16", "fp32"),
+    (8, 131104, 896, 128, "bf16", "relu", None, "bf16"),
+]
 
 
-@pytest.mark.parametrize("shape", sorted({c[:4] for c in GEMM + SPLIT}))
+@pytest.mark.parametrize("shape", sorted({c[:4] for c in GEMM + SPLIT + WIDE}))
 def test_the_shapes_run_the_kernels_they_are_here_for(shape):
     T, N, K, G = shape
-    assert kernel(*shape) == ("gemm" if any(c[:4] == shape for c in GEMM) else "gemm split")
-    assert N % 4 == 0
+    if any(c[:4] == shape for c in WIDE):
+        assert kernel(*shape) == "wide"
+        assert wide_blocks(T, N, K) > 1
+    else:
+        assert kernel(*shape) == ("gemm" if any(c[:4] == shape for c in GEMM) else "gemm split")
+        assert N % 4 == 0
     if shape == (2100, 2048, 4224, 64):
         assert K // G > 64
 
@@ -136,3 +160,20 @@ def pick_rows(layer, d, rows):
     ds = {**d, "bias": None if d["bias"] is None else d["bias"][at],
           "residual": None if d["residual"] is None else d["residual"][:, at].clone()}
     return sub, ds
+
+
+@gpu
+@pytest.mark.parametrize("T,N,K,G,bias,kind,residual,out", WIDE)
+def test_wide_gemv_of_several_blocks_per_wave(T, N, K, G, bias, kind, residual, out):
+    label = f"wide T={T} N={N} K={K} G={G} {bias} {kind} {residual}->{out}"
+    say(label)
+    layer, d = case(T, N, K, G, bias, residual, out, False, seed=N)
+    got = run(d, kind)
+    torch.cuda.synchronize()
+    # a row of every block of 16, each place in turn, and the last blocks whole
+    rows = np.unique(np.concatenate([(np.arange(0, N, 16) + np.arange(-(-N // 16)) % 16).clip(max=N - 1),
+                                     np.arange(max(0, N - 200), N)]))
+    sub, ds = pick_rows(layer, d, rows)
+    want, err = expected(sub, ds, kind)
+    check(got[:, torch.from_numpy(rows).cuda()], want, err, TYPES[out], label)
+    assert bool(torch.isfinite(got).all())
