@@ -12,7 +12,8 @@ import pytest
 import torch
 
 from quantized_moe_router_amd import _binding as B
-from test_gpu_int8_fused import TYPES, case, check, expected, inside, run
+from quantized_moe_router_amd.layer import Int8Linear
+from test_gpu_int8_fused import TYPES, U, case, check, expected, inside, run
 
 gpu = pytest.mark.gpu
 CUS = 256
@@ -177,3 +178,100 @@ def test_wide_gemv_of_several_blocks_per_wave(T, N, K, G, bias, kind, residual, 
     want, err = expected(sub, ds, kind)
     check(got[:, torch.from_numpy(rows).cuda()], want, err, TYPES[out], label)
     assert bool(torch.isfinite(got).all())
+
+
+# ---------------------------------------------------------------------------
+# Every kernel
+# ---------------------------------------------------------------------------
+EVERY = {"rowsplit": (3, 72, 1152, 128), "gemv": (4, 260, 320, 64), "mfma": (9, 260, 320, 64),
+         "wide": (9, 8196, 640, 128), "short": (150, 2600, 320, 64), "kwaves": (70, 260, 1152, 128),
+         "kwaves split": (64, 160, 10240, 64), "gemm": (1100, 1280, 384, 64), "gemm split": (1024, 320, 5120, 64)}
+
+
+@pytest.mark.parametrize("name", EVERY)
+def test_every_kernel_has_a_shape(name):
+    assert kernel(*EVERY[name]) == name
+
+
+@gpu
+@pytest.mark.parametrize("name", EVERY)
+def test_repeated_calls_agree_in_every_bit(name):
+    T, N, K, G = EVERY[name]
+    say(name)
+    _, d = case(T, N, K, G, "fp32", "fp32", "fp32", False, seed=3)
+    first = run(d, "silu").clone()
+    for i in range(20):
+        d["out"].fill_(float(i))
+        if i % 3 == 0:
+            torch.randn(1 << 18, device="cuda").sort()   # other kernels leave LDS and caches otherwise
+        assert torch.equal(run(d, "silu"), first), f"{name}: call {i} differs"
+
+
+def as_fp16_toward_zero(x):
+    """What the activations are taken as: fp16, rounded toward zero, at most
+    65504 in magnitude."""
+    step = np.exp2(np.maximum(np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -60))), -14) - 10)
+    return np.clip(np.trunc(x / step) * step, -65504, 65504)
+
+
+@gpu
+@pytest.mark.parametrize("name", EVERY)
+def test_activations_beyond_the_normal_range_of_fp16(name):
+    T, N, K, G = EVERY[name]
+    say(name)
+    layer, d = case(T, N, K, G, None, None, "fp32", False, seed=11)
+    rng = np.random.default_rng(T)
+    x = d["x"].double().cpu().numpy()
+    x[0] = rng.standard_normal(K) * 2.0 ** -18                      # fp16's subnormal numbers
+    x[1] = np.exp2(rng.uniform(-30, 20, K)) * rng.choice([-1, 1], K)   # all of its range and beyond
+    d["x"] = torch.from_numpy(x).to(torch.bfloat16).cuda()
+    x = d["x"].double().cpu().numpy()
+    got = run(d, "none")
+    torch.cuda.synchronize()
+    toks = np.unique(np.concatenate([[0, 1, 2, T - 1], rng.choice(T, min(T, 20), replace=False)]))
+    rows = np.unique(rng.choice(N, min(N, 600), replace=False))
+    q = layer["packed"][rows].view(np.uint8).astype(np.float64) - 128
+    s = (layer["scales"][rows].astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+    w = q * np.repeat(s, G, axis=1)
+    h = as_fp16_toward_zero(x[toks])
+    # fp16 values this time: only the sums' roundings are left
+    err = (G + 2 * K // G + 32) * U * (np.abs(h) @ np.abs(w).T)
+    check(got[torch.from_numpy(toks).cuda()][:, torch.from_numpy(rows).cuda()], h @ w.T, err, torch.float32, name)
+
+
+@gpu
+@pytest.mark.parametrize("name", EVERY)
+def test_infinities_and_nan_stay_in_their_token(name):
+    T, N, K, G = EVERY[name]
+    say(name)
+    _, d = case(T, N, K, G, None, None, "fp32", False, seed=12)
+    clean = run(d, "none").clone()
+    d["x"][0, 1::7] = math.nan
+    d["x"][T - 1, K - 1] = math.inf
+    got = run(d, "none")
+    torch.cuda.synchronize()
+    assert bool(got[0].isnan().all())
+    assert not bool(torch.isfinite(got[T - 1]).any())    # infinite, or NaN where the code is zero
+    assert torch.equal(got[1:T - 1], clean[1:T - 1])
+
+
+@gpu
+@pytest.mark.parametrize("name", EVERY)
+def test_graph_replays_of_every_kernel_in_place(name):
+    # the residual stream updated in place by replays: out is the residual
+    T, N, K, G = EVERY[name]
+    say(name)
+    _, d = case(T, N, K, G, "bf16", "fp32", "fp32", False, seed=13)
+    lin = Int8Linear(d["packed"], d["scales"], G, bias=d["bias"], activation="gelu_tanh")
+    stream, start = d["residual"].clone(), d["residual"].clone()
+    lin.forward(d["x"], residual=stream, out=stream)
+    stream.copy_(start)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lin.forward(d["x"], residual=stream, out=stream)
+    want = start.clone()
+    for i in range(4):
+        want = lin.forward(d["x"], residual=want, out_dtype=torch.float32)   # eager work between the replays
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(stream, want), f"{name}: replay {i}"
