@@ -287,10 +287,12 @@ typedef struct moe_int8_epilogue {
     int32_t activation;
 } moe_int8_epilogue;
 
-/* moe_int8_linear with bias, activation and residual in its epilogue (the
- * hyper-connection's down projection is followed by a SiLU, its up projection
- * by an addition to the residual stream: section 3.3, "Hyper-connection
- * (decode-04)"), for rows that lie inside wider ones:
+/* moe_int8_linear with bias, activation and residual in its epilogue, for rows
+ * that lie inside wider ones.  Of the hyper-connection's fused kernels
+ * (section 3.3, "Hyper-connection (decode-04)": down projection, inject and
+ * SiLU in one, up projection and gate mix in the other) it takes over the SiLU
+ * at the down projection's store; the inject and the gate mix are not
+ * expressed here, and the residual is a plain addition.
  *   out[t][r] = residual[t][r] + act(sum_i x[t][i] * (byte[r][i] - 128)
  *               * scale[r][i / group] + bias[r])
  * in fp32, rounded once (to nearest even; a value beyond fp16's range becomes
