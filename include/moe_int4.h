@@ -307,7 +307,11 @@ typedef struct moe_int8_epilogue {
  * alignment of their elements only.  out must not overlap x, the weights or
  * the bias; it may be the residual itself (same address, type and stride), and
  * must not overlap it otherwise.
- * Shapes, activations and determinism as in moe_int8_linear.  The workspace
+ * Shapes and determinism as in moe_int8_linear.  So is the range of x: it is
+ * taken as fp16, rounded toward zero (exact for finite bf16 values of magnitude
+ * 2^-14 .. 65504; smaller ones lose low bits, zero below 2^-24; larger ones
+ * count as +-65504), whatever the type of out; an infinity or a NaN of x shows
+ * in its own token's outputs alone.  The workspace
  * (moe_int8_linear_fused_workspace_bytes; NULL when that is 0) needs no
  * clearing and holds nothing between calls; calls in flight at the same time
  * need one each.  The stream must belong to the current device. */
