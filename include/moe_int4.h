@@ -368,7 +368,9 @@ typedef struct moe_int4_logits_rules {
  *   v has a bias:      l = l + bias
  *   temperature > 0:   l = l / temperature
  *   mask bit clear:    l = -infinity, whatever l was (NaN too)
- * in fp32, rounded once to out_type.  A row whose mask leaves nothing comes
+ * in fp32, rounded once to out_type; the quotient by the temperature is a
+ * product with 1 / temperature (up to an ulp of fp32 more) where that lies
+ * within 2^-100 .. 2^100.  A row whose mask leaves nothing comes
  * out as -infinity everywhere.
  *   logits  [rows][vocab] of logits_type, rows logits_stride apart
  *   out     [rows][vocab] of out_type, rows out_stride apart; what lies
