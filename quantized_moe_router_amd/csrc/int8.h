@@ -35,8 +35,10 @@ __device__ __forceinline__ u32x4_t bf16x8_to_f16x8(u32x4_t v)
 //   out[t][r] = rnd(residual[t][r] + act(sum + bias[r]))
 // in fp32, one rounding.  Everything happens on the sum in registers, so the
 // activation and the addition cost no pass over [T][N] of their own.
-// Accurate to a few units of fp32's last place throughout: an fp32 output
-// shows errors that a bf16 one would hide.
+// The activations are accurate to a few units of fp32's last place (an fp32
+// output shows errors that a bf16 one would hide), but for the far negative
+// tails of GELU and its tanh form: there the rounding of the argument of erfc
+// or the exponential moves the result by up to v^2 or 10 |u| units.
 // ---------------------------------------------------------------------------
 // 1 / (1 + e^-z), as t / (1 + t) or 1 / (1 + t) with t = e^-|z| in (0, 1]: no
 // overflow, and a divisor in [1, 2], whose reciprocal is the hardware's with
