@@ -532,7 +532,7 @@ struct Int8Plan {
     int mtiles, ntiles, ksplit, kslice;
     size_t pstride;      // floats per split in the partials (T * N rounded up to 4)
     size_t part_bytes;   // fp32 split-K partials (workspace)
-    bool wide;           // fused variant: matrix-core GEMV with whole-line loads (5..16 tokens)
+    bool wide;           // fused variant: matrix-core GEMV with whole-line loads (int8_fused_plan says when)
     bool kwaves;         // fused variant: K over the waves of a workgroup
 };
 Int8Plan int8_plan(int T, int N, int K, int G);

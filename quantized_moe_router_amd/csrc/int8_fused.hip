@@ -6,7 +6,8 @@
 //   * int8_ksplit_kernel: more than four tokens and few 32 x 32 output tiles
 //     (the down projection): the waves of one workgroup split K and meet in
 //     LDS, so no partial sum goes through memory;
-//   * int8_gemv_wide_kernel: 3 or 5 to 16 tokens on wide matrices (lm_head).
+//   * int8_gemv_wide_kernel: few tokens on wide matrices (lm_head): up to 16,
+//     from 5 on, or from 3 on where N * K >= kInt8WideMinWeights.
 //
 // The first two use v_mfma_f32_32x32x16_f16 on exact fp16 codes and activations, a
 // group's sum starting from zero and folded into the accumulator with the
@@ -446,7 +447,7 @@ __global__ __launch_bounds__(64 * kKwWaves) void int8_ksplit_kernel(FusedArgs g)
 }
 
 // ---------------------------------------------------------------------------
-// 5 to 16 tokens on wide matrices (lm_head): one read of the weights at the
+// Few tokens on wide matrices (lm_head): one read of the weights at the
 // memory's rate.  A wave owns 16 weight rows at a time.  Per step of 128 inputs
 // eight lanes load the 128 consecutive bytes of a row, and the 16 x 128 block
 // passes through LDS of the wave's own into the B operand of
