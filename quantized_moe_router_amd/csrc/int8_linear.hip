@@ -1171,17 +1171,28 @@ hipError_t launch_int8_linear(const uint16_t *x, const int32_t *wq, const uint16
 // on large ones from 3 tokens (4 tokens: 248320 x 2560 107 us against
 // int8_gemv_kernel's 136, 32000 x 4096 28 against 33, but 10240 x 2560 13
 // against 11; 2 tokens gain nothing), and for few output tiles of 32 x 32
-// K goes over the waves of a workgroup (measured with int8_gemm_kernel's time
-// behind: N = 320, K = 10240: 32 tokens 8.1 us, 10.9; 512 tokens, 160 tiles,
-// 19.4, 21.8; 1024 tokens, 320 tiles, 36.0, 29.6; N = 1003, K = 1152: 77
-// tokens 6.3, 12.4; 512 tokens, 512 tiles, 12.7, 19.5).  A K of many stages
-// per wave is split over workgroups too where the tiles leave most CUs idle:
-// 32 tokens of N = 320, K = 10240 take 17.9 us unsplit, 8.1 in 16 parts; from
-// K = 5120 that pays for the second launch.  Of the short K's, those of three
-// groups or more that take it: 150 x 1295 x 320 with GELU 7.8 us against 15.4,
-// 64 x 1280 x 192 with SiLU 8.0 against 10.0; of 320 tiles on int8_short_fused_kernel
-// is faster (17 x 10240 x 192 8.1 us against 9.2), and for one or two groups,
-// where a workgroup has as few waves (64 x 1280 x 64 9.3 against 12.0).
+// K goes over the waves of a workgroup.  Both sides, in replayed graphs, with
+// SiLU and a bf16 residual (us with K over the waves, us of int8_gemm_kernel;
+// N = 1024, group 64):
+//   tiles       256          512          544          768         1024
+//   K  384   5.6, 21.4    9.7, 21.5   13.6, 21.7   14.1, 21.7   18.3, 21.8
+//   K 1280   7.1, 14.0   12.2, 17.4   16.8, 18.1   17.3, 20.9   22.3, 22.4
+//   K 2560  10.3, 17.6   17.0, 22.4   23.3, 22.6   24.0, 25.7   30.8, 25.7
+//   K 2688  10.0, 17.6   16.9, 21.6   22.6, 22.5   23.3, 26.3   30.2, 25.3
+//   K 3584  11.4, 20.2   20.3, 23.7   27.1, 24.7   29.4, 27.8   37.2, 27.8
+//   K 5120  13.8, 22.3   25.4, 26.1   34.8, 28.4   37.4, 31.6   48.8, 31.2
+//   K 10240 22.5, 25.0   43.1, 31.4   58.1, 40.2   63.0, 45.2   81.7, 45.1
+// (group 128: a quarter slower over the waves at K = 384, a tenth from 1280 on,
+// int8_gemm_kernel as here).  The border of 512 tiles could so go on to K =
+// 3584, and for K up to 1280 lie beyond 512: 10 to 60 % of such a call.
+// A K of many stages per wave is split over workgroups too where the tiles
+// leave most CUs idle: N = 320, 32 tokens, unsplit and split: K = 10240 18.6 us,
+// 8.5 in 10 parts; K = 5120 9.4, 7.6 in 5; K = 4096 8.4, 7.6 in 4; K = 2560
+// 7.4, 8.3 in 2.  Of the short K's, those of three groups or more take it, up to
+// 256 tiles (against int8_short_fused_kernel): 64 x 1280 x 192 6.4 us, 10.0;
+// 256 x 1024 x 320 6.0, 11.3; of 512 tiles 11.7, 10.1 and 10.7, 11.4.  One
+// group is one wave to a workgroup: 64 x 1280 x 64 10.8, 9.0.  (Two groups
+// would gain too: 64 x 1280 x 128 7.3, 9.7.)
 Int8Plan int8_fused_plan(int T, int N, int K, int G)
 {
     Int8Plan p = int8_plan(T, N, K, G);
