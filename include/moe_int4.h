@@ -252,6 +252,8 @@ int32_t moe_int4_quantize(const uint16_t *w, int32_t rows, int32_t cols, int32_t
  * and tokens * k below 2^31; tokens = 0 is a no-op.  Pointers must be
  * 16-byte aligned; the workspace may be NULL when
  * moe_int8_linear_workspace_bytes reports 0 for the same shape.
+ * (moe_int8_linear_fused without an epilogue is the same product, and faster
+ * for 3 to 16 tokens of a large matrix: 8 of [248320, 2560] 114 us, here 152.)
  * Asynchronous on hip_stream; no allocation, no host synchronisation. */
 int32_t moe_int8_linear_workspace_bytes(int32_t tokens, int32_t n, int32_t k, int32_t group,
                                         size_t *bytes);
