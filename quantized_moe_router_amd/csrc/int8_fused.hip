@@ -306,11 +306,15 @@ __global__ __launch_bounds__(kSpThreads, 3) void int8_short_fused_kernel(FusedAr
 // no partial sum goes through memory, unless K is split over workgroups too
 // (gridDim.y) because the tiles alone would leave CUs idle.
 //
-// What bounds it: the vector instructions of a stage (115 per wave: half of
-// them convert activations, which the ten weight-row tiles of a mixer repeat)
-// and their latencies; [320, 10240] at 512 tokens takes 19 us (3.4 GFLOP).
-// Tiles of 64 x 64, which halve the conversions, leave 40 workgroups, and with
-// K over six workgroups each take as long.
+// What bounds it: no one unit.  [320, 10240] at 512 tokens takes 19 us (3.4
+// GFLOP) in 160 workgroups, each alone on its CU (the LDS is reserved for 16
+// waves, 128 KB, however many there are), so 96 CUs idle.  On the others the
+// vector ALU issues half of the time (32 instructions to an MFMA: a stage
+// converts 32 x 64 activations, which the ten weight-row tiles of a mixer
+// repeat, and folds 16 sums), the matrix cores work an eighth of it, and a wave
+// waits for data or a barrier two fifths of it.  Tiles of 64 x 64, which halve
+// the conversions, leave 40 workgroups, and with K over six workgroups each
+// take as long.
 // ---------------------------------------------------------------------------
 constexpr int kKwWaves = 16;
 constexpr int kKwTile = 32;
