@@ -383,10 +383,11 @@ typedef struct moe_int4_logits_rules {
  * 2^34, widths in [0, 2^24], strides at most 2^24; with one row they are not
  * read.
  * Pointers need the alignment of their elements only, but where a row of the
- * history, the logits or out does not begin on 16 bytes (with several rows: a
- * stride of no whole multiple), every row of that operand is taken an element
- * at a time: a history of 131071 ids in two rows takes 24 us, one of 131072 12;
- * 256 rows of 50257 logits 33 us, of 50256 16.  Needs no workspace.
+ * history, the logits or out does not begin on 16 bytes (8 for 16-bit logits
+ * or out beside fp32 ones; with several rows: a stride of no whole multiple),
+ * every row of that operand is taken an element at a time: a history of 131071
+ * ids in two rows takes 24 us, one of 131072 12; 256 rows of 50257 logits 33
+ * us, of 50256 16.  Needs no workspace.
  * The result does not depend on the order in which the history is counted.
  * The stream must belong to the current device. */
 int32_t moe_int4_logits_process(const void *logits, int32_t logits_type, int64_t logits_stride,

@@ -22,12 +22,12 @@
 // (with branches the same call took 63 us).  The temperature is one product
 // with its inverse: the quotient's ten instructions cost as much as the rest.
 //
-// Rows that do not all begin on 16 bytes are taken an element at a time: the
-// logits and out by each lane's own 4 or 8 (256 x 50257 bf16 with a mask 33 us,
-// 256 x 50256 16), the history without any id on its way while one is counted
-// (2 rows of 248320 with 131071 ids each 24 us, with 131072 12; where the
-// history is short beside the logits it hides: 64 rows with 4097 ids 24, with
-// 4096 22).
+// Rows that do not all begin on 16 bytes (8 where a lane's four elements are 16
+// bits wide) are taken an element at a time: the logits and out by each lane's
+// own 4 or 8 (256 x 50257 bf16 with a mask 33 us, 256 x 50256 16), the history
+// without any id on its way while one is counted (2 rows of 248320 with 131071
+// ids each 24 us, with 131072 12; where the history is short beside the logits
+// it hides: 64 rows with 4097 ids 24, with 4096 22).
 #include "common.h"
 
 namespace moe {
