@@ -274,7 +274,8 @@ int32_t moe_int8_linear(const uint16_t *x, const int32_t *w_packed, const uint16
 #define MOE_ACT_GELU_TANH 4  /* v / (1 + e^-2u), u = sqrt(2/pi) (v + 0.044715 v^3) */
 #define MOE_ACT_SIGMOID 5    /* 1 / (1 + e^-v) */
 
-/* What moe_int8_linear_fused does to a row of products before its one store.
+/* What moe_int8_linear_fused and the INT4 linear layers do to a row of products
+ * before its one store.
  *   bias      [n] of bias_type, or NULL
  *   residual  [tokens][n] of residual_type, rows residual_stride elements
  *             apart, or NULL
@@ -393,6 +394,148 @@ typedef struct moe_int4_logits_rules {
 int32_t moe_int4_logits_process(const void *logits, int32_t logits_type, int64_t logits_stride,
                            int32_t rows, int32_t vocab, const moe_int4_logits_rules *rules, void *out,
                            int32_t out_type, int64_t out_stride, void *hip_stream);
+
+/* INT4 W4A16 linear layer: the product with a matrix as moe_int4_quantize
+ * writes it (a draft head's projections, "Running 125B MoE on Three 3090s -
+ * vLLM Optimization Edition", section 7), with the epilogue of
+ * moe_int8_linear_fused.
+ *   out[t][r] = residual[t][r] + act(sum_i x[t][i] * code[r][i]
+ *               * scale[r][i / group] + bias[r])
+ * in fp32, rounded once (to nearest even; a value beyond fp16's range becomes
+ * infinite) to out_type.
+ *   x         bf16  [tokens][k], rows x_stride elements apart: x_stride >= k,
+ *                   a multiple of 8
+ *   w_packed  int32 [n][k/8], w_scales bf16 [n][k/group]
+ *   out       [tokens][n] of out_type, rows out_stride >= n elements apart;
+ *             what lies between the rows is left as it was
+ *   epilogue  may be NULL (out is then the plain product)
+ * x is taken as bf16 unchanged.  Products are formed as x * (code + 24) less
+ * 24 * x, exactly, and summed in fp32 group by group: values of x beyond 2^110
+ * may overflow on the way, and a token with an infinity or a NaN in x has NaN
+ * in all its own outputs (before activation and residual), and in no others.
+ * group is 64 or 128, k a multiple of it (at most 65536), n in [1, 2^24],
+ * tokens in [0, 2^20] with tokens * n and tokens * k below 2^31; tokens = 0 is
+ * a no-op.  Strides, alignment, overlaps, workspace and streams as in
+ * moe_int8_linear_fused.  The result does not depend on timing. */
+int32_t moe_int4_linear_workspace_bytes(int32_t tokens, int32_t n, int32_t k, int32_t group,
+                                        size_t *bytes);
+int32_t moe_int4_linear(const uint16_t *x, int64_t x_stride, const int32_t *w_packed,
+                        const uint16_t *w_scales, int32_t tokens, int32_t n, int32_t k,
+                        int32_t group, const moe_int8_epilogue *epilogue, void *out,
+                        int32_t out_type, int64_t out_stride, void *workspace,
+                        size_t workspace_bytes, void *hip_stream);
+
+/* Rows grouped by expert, as moe_int4_route answers them.  Place p of the
+ * sorted order belongs to expert e where offsets[e] <= p < offsets[e + 1].
+ * Tables are device memory (int32 and fp32, aligned to their elements):
+ *   offsets      [experts + 1], not decreasing, between 0 and places.  Places
+ *                before offsets[0] and from offsets[experts] on belong to no
+ *                expert: their rows of out are left as they were.
+ *   gather       [places] or NULL: place p reads row gather[p] / gather_div of
+ *                x (a slot's token, with gather_div = top_k); NULL: row p.  A
+ *                row outside [0, x_rows) counts as zeros.
+ *   scatter      [places] or NULL: place p writes row scatter[p] of out; NULL:
+ *                row p.  A row outside [0, out_rows) is not written; of two
+ *                places that name the same row either may stand in each element.
+ *   row_weights  [out_rows] or NULL: a factor for each row of out
+ * Offsets that decrease or pass places reach no memory outside the operands,
+ * but which rows they compute is not defined. */
+typedef struct moe_int4_groups {
+    const int32_t *offsets;
+    const int32_t *gather;
+    const int32_t *scatter;
+    const float *row_weights;
+    int32_t experts;
+    int32_t places;
+    int32_t gather_div;
+    int32_t x_rows;
+    int32_t out_rows;
+} moe_int4_groups;
+
+/* INT4 products grouped by expert ("MoE block (decode-05)": the routed experts
+ * are a W4A16 grouped GEMM over the permuted tokens), one product at a time:
+ * for each place p of expert e, with i and o its rows of x and of out,
+ *   out[o][r] = residual[o][r] + row_weights[o] * act(sum_h x[i][h]
+ *               * code[e][r][h] * scale[e][r][h / group] + bias[e][r])
+ *   x         bf16  [x_rows][k]; w_packed int32 [experts][n][k/8],
+ *             w_scales bf16 [experts][n][k/group]
+ *   out       [out_rows][n] of out_type
+ *   epilogue  may be NULL; its bias is [experts][n], its residual [out_rows][n]
+ * experts in [1, 1024], places, x_rows and out_rows in [0, 2^20], each times n
+ * (x_rows: times k) below 2^31; places = 0 is a no-op.  Without gather x has
+ * at least places rows, without scatter so has out; a residual that is out
+ * itself needs scatter to name no row twice.  Otherwise as moe_int4_linear. */
+int32_t moe_int4_grouped_linear_workspace_bytes(const moe_int4_groups *groups, int32_t n,
+                                                int32_t k, int32_t group, size_t *bytes);
+int32_t moe_int4_grouped_linear(const uint16_t *x, int64_t x_stride, const int32_t *w_packed,
+                                const uint16_t *w_scales, const moe_int4_groups *groups,
+                                int32_t n, int32_t k, int32_t group,
+                                const moe_int8_epilogue *epilogue, void *out, int32_t out_type,
+                                int64_t out_stride, void *workspace, size_t workspace_bytes,
+                                void *hip_stream);
+
+/* Drafted tokens of a batch of sequences, to be verified against the target's
+ * logits (the step behind the draft head, section 7).  Sequence b drafted
+ * lengths[b] tokens; the target has answered a row of logits for each of them
+ * and one behind the last, the draft head one for each.  Device memory:
+ *   target   [seqs * (width + 1)][vocab] of target_type, rows target_stride
+ *            apart: row b * (width + 1) + i for draft i of sequence b
+ *   draft    [seqs * width][vocab] of draft_type, rows draft_stride apart, or
+ *            NULL: each draft had probability one (found by lookup)
+ *   tokens   int32 [seqs][width]   the drafted tokens
+ *   lengths  int32 [seqs] or NULL (all width), taken as clamped to [0, width]
+ *   coins    fp32 [seqs][width]    random numbers in [0, 1)
+ *   picks    fp32 [seqs]           random numbers in [0, 1)
+ *   temperature  fp32 [seqs] or NULL: a sequence whose temperature is not
+ *            above zero is greedy; others take the logits as they are (the
+ *            rules on logits have scaled them)
+ * Both kinds of logits come as moe_int4_logits_process leaves them; -infinity
+ * marks a token that is not allowed, and NaN counts as that. */
+typedef struct moe_int4_drafts {
+    const void *target;
+    const void *draft;
+    const int32_t *tokens;
+    const int32_t *lengths;
+    const float *coins;
+    const float *picks;
+    const float *temperature;
+    int64_t target_stride;
+    int64_t draft_stride;
+    int32_t target_type;
+    int32_t draft_type;
+    int32_t seqs;
+    int32_t width;
+    int32_t vocab;
+} moe_int4_drafts;
+
+/* Verifies them.  With p_i and q_i the softmax of target and draft rows i (of a
+ * row with +infinities these share its probability; a row without a logit above
+ * -infinity has zeros) and x_i draft i:
+ *   draft i is accepted while coins[i] * q_i(x_i) < p_i(x_i); the first that is
+ *   not ends the sequence, and so does the last draft.  n of them accepted:
+ *   r = max(0, p_n - q_n), or p_n behind the last draft or where that is zero
+ *   everywhere; the next token is the first v whose r_0 + .. + r_v exceeds
+ *   picks * (the sum of all r), or -1 where p_n is zero everywhere.
+ *   A greedy sequence accepts a draft that is the first of the largest target
+ *   logits, and goes on with that token.
+ *   accepted    int32 [seqs]             out  n
+ *   out_tokens  int32 [seqs][width + 1]  out  the n accepted drafts, the next
+ *               token, and -1 behind it
+ * Drafts outside [0, vocab) have probability zero.  Probabilities and their
+ * sums are formed in 64 bits, so that the token is the definition's but for
+ * picks within about 2^-40 of a border.  width = 0 draws each sequence's next
+ * token.  seqs in [0, 65536] (0 is a no-op), width in [0, 64], vocab in
+ * [1, 2^24], seqs * (2 width + 1) at most 2^20 and with vocab at most 2^36;
+ * strides from vocab to 2^24.  Pointers need the alignment of their elements
+ * only.  out_tokens and accepted must not overlap each other, the workspace or
+ * what is read.  The workspace (16-byte aligned) needs no clearing and holds
+ * nothing between calls; calls in flight at the same time need one each.
+ * Nothing depends on timing.  The stream must belong to the current device. */
+int32_t moe_int4_verify_drafts_workspace_bytes(int32_t seqs, int32_t width, int32_t vocab,
+                                               size_t *bytes);
+int32_t moe_int4_verify_drafts(const moe_int4_drafts *drafts, int32_t *accepted,
+                               int32_t *out_tokens, void *workspace, size_t workspace_bytes,
+                               void *hip_stream);
 
 /* Message for the calling thread's most recent failing call ("" if none). */
 const char *moe_int4_last_error(void);

@@ -43,6 +43,17 @@ class MoeLogitsRules(ctypes.Structure):
                 + [("history_width", _c_i32), ("bias_width", _c_i32)])
 
 
+class MoeGroups(ctypes.Structure):
+    _fields_ = ([(f, _c_void_p) for f in ("offsets", "gather", "scatter", "row_weights")]
+                + [(f, _c_i32) for f in ("experts", "places", "gather_div", "x_rows", "out_rows")])
+
+
+class MoeDrafts(ctypes.Structure):
+    _fields_ = ([(f, _c_void_p) for f in ("target", "draft", "tokens", "lengths", "coins", "picks", "temperature")]
+                + [(f, ctypes.c_int64) for f in ("target_stride", "draft_stride")]
+                + [(f, _c_i32) for f in ("target_type", "draft_type", "seqs", "width", "vocab")])
+
+
 class MoeError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"moe_int4 error {code}: {msg}")
@@ -74,13 +85,23 @@ def lib() -> ctypes.CDLL:
         L.moe_int8_linear_fused.argtypes = [P, c_i64, P, P] + [_c_i32] * 4 + [P, P, _c_i32, c_i64, P,
                                                                              ctypes.c_size_t, P]
         L.moe_int4_logits_process.argtypes = [P, _c_i32, c_i64, _c_i32, _c_i32, P, P, _c_i32, c_i64, P]
+        size_p = ctypes.POINTER(ctypes.c_size_t)
+        L.moe_int4_linear_workspace_bytes.argtypes = [_c_i32] * 4 + [size_p]
+        L.moe_int4_linear.argtypes = [P, c_i64, P, P] + [_c_i32] * 4 + [P, P, _c_i32, c_i64, P, ctypes.c_size_t, P]
+        L.moe_int4_grouped_linear_workspace_bytes.argtypes = [P] + [_c_i32] * 3 + [size_p]
+        L.moe_int4_grouped_linear.argtypes = [P, c_i64, P, P, P] + [_c_i32] * 3 + [P, P, _c_i32, c_i64, P,
+                                                                                 ctypes.c_size_t, P]
+        L.moe_int4_verify_drafts_workspace_bytes.argtypes = [_c_i32] * 3 + [size_p]
+        L.moe_int4_verify_drafts.argtypes = [P, P, P, P, ctypes.c_size_t, P]
         L.moe_int4_last_error.restype = ctypes.c_char_p
         L.moe_int4_version.restype = ctypes.c_char_p
         for f in ("moe_int4_workspace_bytes", "moe_int4_route", "moe_int4_experts", "moe_int4_forward",
                   "moe_int4_forward_traced", "moe_int4_forward_noalloc", "moe_int4_quantize",
                   "moe_int8_linear_workspace_bytes", "moe_int8_linear",
                   "moe_int8_linear_fused_workspace_bytes", "moe_int8_linear_fused",
-                  "moe_int4_logits_process"):
+                  "moe_int4_logits_process", "moe_int4_linear_workspace_bytes", "moe_int4_linear",
+                  "moe_int4_grouped_linear_workspace_bytes", "moe_int4_grouped_linear",
+                  "moe_int4_verify_drafts_workspace_bytes", "moe_int4_verify_drafts"):
             getattr(L, f).restype = _c_i32
         _lib = L
     return _lib
@@ -92,6 +113,9 @@ EXPORTED = ("moe_int4_workspace_bytes", "moe_int4_route", "moe_int4_experts",
             "moe_int8_linear_workspace_bytes", "moe_int8_linear",
             "moe_int8_linear_fused_workspace_bytes", "moe_int8_linear_fused",
             "moe_int4_logits_process",
+            "moe_int4_linear_workspace_bytes", "moe_int4_linear",
+            "moe_int4_grouped_linear_workspace_bytes", "moe_int4_grouped_linear",
+            "moe_int4_verify_drafts_workspace_bytes", "moe_int4_verify_drafts",
             "moe_int4_last_error", "moe_int4_version")
 
 
@@ -376,6 +400,169 @@ def moe_int4_logits_process(logits, rules: MoeLogitsRules, out, stream=None):
             return moe_int4_logits_process(logits, rules, out, stream)
     rc = lib().moe_int4_logits_process(logits.data_ptr(), in_type, stride, rows, vocab, ctypes.byref(rules),
                                        out.data_ptr(), out_type, out_stride, _stream_on(stream, index))
+    if rc:
+        _check(rc)
+
+
+def moe_int4_linear_workspace_bytes(tokens: int, n: int, k: int, group: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check(lib().moe_int4_linear_workspace_bytes(int(tokens), int(n), int(k), int(group), ctypes.byref(b)))
+    return b.value
+
+
+def check_int4_weights(w_packed, w_scales, shape: tuple, k: int, group: int):
+    """The codes and scales of an INT4 matrix [n, k] (or of one for each expert,
+    [experts, n, k]; shape: all but k)."""
+    import torch
+    if w_packed.dtype != torch.int32 or w_packed.shape != (*shape, k // 8) or not w_packed.is_contiguous():
+        raise ValueError(f"w_packed is {w_packed.dtype} {tuple(w_packed.shape)}, expected contiguous int32 "
+                         f"{(*shape, k // 8)}")
+    if group <= 0 or k % group or type_code(w_scales.dtype) != TYPE_BF16 or w_scales.shape != (*shape, k // group) \
+            or not w_scales.is_contiguous():
+        raise ValueError(f"w_scales is {w_scales.dtype} {tuple(w_scales.shape)}, expected contiguous bfloat16 "
+                         f"{tuple(shape)} x {k} / {group}")
+
+
+def _epilogue(bias, bias_shape: tuple, residual, rows: int, n: int, activation: str) -> MoeInt8Epilogue:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation {activation!r} is none of {', '.join(ACTIVATIONS)}")
+    e = MoeInt8Epilogue(None, None, 0, 0, 0, act)
+    if bias is not None:
+        if bias.shape != bias_shape or not bias.is_contiguous():
+            raise ValueError(f"bias is {tuple(bias.shape)}, expected {bias_shape}, contiguous")
+        e.bias, e.bias_type = bias.data_ptr(), type_code(bias.dtype)
+    if residual is not None:
+        e.residual_stride = row_stride(residual, "residual", rows, n)
+        e.residual, e.residual_type = residual.data_ptr(), type_code(residual.dtype)
+    return e
+
+
+def _check_contiguous(workspace):
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError(f"workspace is {tuple(workspace.shape)} with strides {workspace.stride()}, expected contiguous")
+
+
+def moe_int4_linear(x, w_packed, w_scales, tokens: int, n: int, k: int, group: int, out, bias=None, residual=None,
+                    activation: str = "none", workspace=None, stream=None):
+    """out [tokens, n] = residual + act(x W^T + bias): x bf16 [tokens, k],
+    w_packed int32 [n, k/8], w_scales bf16 [n, k/group], the rest as in
+    moe_int8_linear_fused.  workspace: uint8, may be None when the shape needs
+    none."""
+    check_int4_weights(w_packed, w_scales, (n,), k, group)
+    int4_linear(x, w_packed, w_scales, tokens, n, k, group, out, bias, residual, activation, workspace, stream)
+
+
+def int4_linear(x, w_packed, w_scales, tokens: int, n: int, k: int, group: int, out, bias, residual,
+                activation: str, workspace, stream=None):
+    """moe_int4_linear on weights that have passed check_int4_weights."""
+    if type_code(x.dtype) != TYPE_BF16:
+        raise ValueError(f"x is {x.dtype}, expected bfloat16 (or its bits)")
+    x_stride, out_stride = row_stride(x, "x", tokens, k), row_stride(out, "out", tokens, n)
+    out_type = type_code(out.dtype)
+    e = _epilogue(bias, (n,), residual, tokens, n, activation)
+    _check_contiguous(workspace)
+    index = device_index(x, "x")
+    if index != _current_device():
+        with _device(index):
+            return int4_linear(x, w_packed, w_scales, tokens, n, k, group, out, bias, residual, activation,
+                               workspace, stream)
+    for name, t in (("w_packed", w_packed), ("w_scales", w_scales), ("out", out), ("bias", bias),
+                    ("residual", residual), ("workspace", workspace)):
+        if t is not None:
+            device_index(t, name, index)
+    rc = lib().moe_int4_linear(x.data_ptr(), x_stride, w_packed.data_ptr(), w_scales.data_ptr(), tokens, n, k, group,
+                               ctypes.byref(e), out.data_ptr(), out_type, out_stride, _ptr(workspace),
+                               0 if workspace is None else workspace.nbytes, _stream_on(stream, index))
+    if rc:
+        _check(rc)
+
+
+def make_groups(x_rows: int, out_rows: int, places: int, offsets, gather=None, gather_div: int = 1, scatter=None,
+                row_weights=None) -> MoeGroups:
+    """The tables of a grouped product (device tensors, which the caller keeps
+    alive): offsets int32 [experts + 1], gather and scatter int32 [places],
+    row_weights fp32 [out_rows] (of any shape of that many)."""
+    import torch
+    for name, t, dtype, count in (("offsets", offsets, torch.int32, None), ("gather", gather, torch.int32, places),
+                                  ("scatter", scatter, torch.int32, places),
+                                  ("row_weights", row_weights, torch.float32, out_rows)):
+        if t is None:
+            continue
+        if t.dtype != dtype or not t.is_contiguous() or (count is not None and t.numel() != count):
+            raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected contiguous {dtype}"
+                             + ("" if count is None else f" of {count}"))
+    return MoeGroups(_ptr(offsets), _ptr(gather), _ptr(scatter), _ptr(row_weights), offsets.numel() - 1, int(places),
+                     int(gather_div), int(x_rows), int(out_rows))
+
+
+def moe_int4_grouped_linear_workspace_bytes(groups: MoeGroups, n: int, k: int, group: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check(lib().moe_int4_grouped_linear_workspace_bytes(ctypes.byref(groups), int(n), int(k), int(group),
+                                                         ctypes.byref(b)))
+    return b.value
+
+
+def moe_int4_grouped_linear(x, w_packed, w_scales, groups: MoeGroups, n: int, k: int, group: int, out, bias=None,
+                            residual=None, activation: str = "none", workspace=None, stream=None):
+    """out = residual + row_weights act(x W_e^T + bias_e) over the places of
+    each expert e: x bf16 [x_rows, k], w_packed int32 [experts, n, k/8],
+    w_scales bf16 [experts, n, k/group], bias [experts, n], out and residual
+    [out_rows, n].  groups: make_groups on x's device."""
+    check_int4_weights(w_packed, w_scales, (groups.experts, n), k, group)
+    int4_grouped_linear(x, w_packed, w_scales, groups, n, k, group, out, bias, residual, activation, workspace, stream)
+
+
+def int4_grouped_linear(x, w_packed, w_scales, groups: MoeGroups, n: int, k: int, group: int, out, bias, residual,
+                        activation: str, workspace, stream=None):
+    """moe_int4_grouped_linear on weights that have passed check_int4_weights."""
+    if type_code(x.dtype) != TYPE_BF16:
+        raise ValueError(f"x is {x.dtype}, expected bfloat16 (or its bits)")
+    x_stride, out_stride = row_stride(x, "x", groups.x_rows, k), row_stride(out, "out", groups.out_rows, n)
+    out_type = type_code(out.dtype)
+    e = _epilogue(bias, (groups.experts, n), residual, groups.out_rows, n, activation)
+    _check_contiguous(workspace)
+    index = device_index(x, "x")
+    if index != _current_device():
+        with _device(index):
+            return int4_grouped_linear(x, w_packed, w_scales, groups, n, k, group, out, bias, residual, activation,
+                                       workspace, stream)
+    for name, t in (("w_packed", w_packed), ("w_scales", w_scales), ("out", out), ("bias", bias),
+                    ("residual", residual), ("workspace", workspace)):
+        if t is not None:
+            device_index(t, name, index)
+    rc = lib().moe_int4_grouped_linear(x.data_ptr(), x_stride, w_packed.data_ptr(), w_scales.data_ptr(),
+                                       ctypes.byref(groups), n, k, group, ctypes.byref(e), out.data_ptr(), out_type,
+                                       out_stride, _ptr(workspace), 0 if workspace is None else workspace.nbytes,
+                                       _stream_on(stream, index))
+    if rc:
+        _check(rc)
+
+
+def moe_int4_verify_drafts_workspace_bytes(seqs: int, width: int, vocab: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check(lib().moe_int4_verify_drafts_workspace_bytes(int(seqs), int(width), int(vocab), ctypes.byref(b)))
+    return b.value
+
+
+def moe_int4_verify_drafts(drafts: MoeDrafts, accepted, out_tokens, workspace, stream=None):
+    """Verifies drafts (device addresses, which the caller keeps alive;
+    layer.DraftVerifier makes them and checks their shapes) into accepted int32
+    [seqs] and out_tokens int32 [seqs, width + 1]."""
+    import torch
+    for name, t, shape in (("accepted", accepted, (drafts.seqs,)),
+                           ("out_tokens", out_tokens, (drafts.seqs, drafts.width + 1))):
+        if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected contiguous int32 {shape}")
+    _check_contiguous(workspace)
+    index = device_index(accepted, "accepted")
+    device_index(out_tokens, "out_tokens", index)
+    device_index(workspace, "workspace", index)
+    if index != _current_device():
+        with _device(index):
+            return moe_int4_verify_drafts(drafts, accepted, out_tokens, workspace, stream)
+    rc = lib().moe_int4_verify_drafts(ctypes.byref(drafts), accepted.data_ptr(), out_tokens.data_ptr(),
+                                      workspace.data_ptr(), workspace.nbytes, _stream_on(stream, index))
     if rc:
         _check(rc)
 

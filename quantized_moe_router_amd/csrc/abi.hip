@@ -798,4 +798,266 @@ int32_t moe_int4_logits_process(const void *logits, int32_t logits_type, int64_t
     return launched(launch_logits(a, logits_type, out_type, (hipStream_t)hip_stream), "logits");
 }
 
+// ---- INT4 linear layer, products grouped by expert ----
+
+static bool overlaps_any(const Rows &o, std::initializer_list<Rows> others, const char **which)
+{
+    for (const Rows &r : others)
+        if (r.p && r.rows > 0 && r.cols > 0 && may_overlap(o, r)) {
+            *which = r.name;
+            return true;
+        }
+    return false;
+}
+
+static int32_t check_int4_matrix(int32_t n, int32_t k, int32_t group)
+{
+    if (group != 64 && group != 128)
+        return fail(MOE_INT4_EINVAL, "group=%d, INT4 supports 64 and 128", group);
+    if (n <= 0 || n > (1 << 24)) return fail(MOE_INT4_EINVAL, "n=%d outside [1, 16777216]", n);
+    if (k <= 0 || k % group || k > 65536)
+        return fail(MOE_INT4_EINVAL, "k=%d must be a positive multiple of group=%d, at most 65536", k, group);
+    return MOE_INT4_OK;
+}
+
+static int32_t check_int4_rows(const char *name, int32_t rows, int32_t cols)
+{
+    if (rows < 0 || rows > (1 << 20)) return fail(MOE_INT4_EINVAL, "%s=%d outside [0, 1048576]", name, rows);
+    if ((long long)rows * cols >= (1LL << 31))
+        return fail(MOE_INT4_EINVAL, "%s times the row's length must stay below 2^31", name);
+    return MOE_INT4_OK;
+}
+
+// The sizes of a call, from which its plan and workspace follow.
+static int32_t int4_sizes(const moe_int4_groups *g, int32_t tokens, int32_t n, int32_t k, int32_t group, Int4Args *a)
+{
+    int32_t rc = check_int4_matrix(n, k, group);
+    if (rc) return rc;
+    *a = Int4Args{};
+    a->N = n;
+    a->K = k;
+    a->G = group;
+    a->experts = a->gather_div = 1;
+    if (!g) {
+        if ((rc = check_int4_rows("tokens", tokens, n)) || (rc = check_int4_rows("tokens", tokens, k))) return rc;
+        a->places = a->x_rows = a->out_rows = tokens;
+        return MOE_INT4_OK;
+    }
+    if (g->experts < 1 || g->experts > kMaxExperts)
+        return fail(MOE_INT4_EINVAL, "experts=%d outside [1, %d]", g->experts, kMaxExperts);
+    if ((rc = check_int4_rows("places", g->places, n)) || (rc = check_int4_rows("out_rows", g->out_rows, n)) ||
+        (rc = check_int4_rows("x_rows", g->x_rows, k)) || (rc = check_int4_rows("places", g->places, k)))
+        return rc;
+    if (g->gather && g->gather_div < 1) return fail(MOE_INT4_EINVAL, "gather_div=%d must be positive", g->gather_div);
+    if (g->places > 0 && g->x_rows < (g->gather ? 1 : g->places))
+        return fail(MOE_INT4_EINVAL, "x_rows=%d, %d places need %d", g->x_rows, g->places, g->gather ? 1 : g->places);
+    if (g->places > 0 && g->out_rows < (g->scatter ? 1 : g->places))
+        return fail(MOE_INT4_EINVAL, "out_rows=%d, %d places need %d", g->out_rows, g->places, g->scatter ? 1 : g->places);
+    a->experts = g->experts;
+    a->places = g->places;
+    a->x_rows = g->x_rows;
+    a->out_rows = g->out_rows;
+    if (g->gather) a->gather_div = g->gather_div;
+    a->offsets = g->offsets;
+    a->gather = g->gather;
+    a->scatter = g->scatter;
+    a->row_weights = g->row_weights;
+    return MOE_INT4_OK;
+}
+
+static int32_t int4_call(Int4Args &a, const uint16_t *x, int64_t x_stride, const int32_t *w_packed,
+                         const uint16_t *w_scales, const moe_int8_epilogue *epilogue, void *out, int32_t out_type,
+                         int64_t out_stride, void *workspace, size_t workspace_bytes, hipStream_t st)
+{
+    int32_t rc;
+    const moe_int8_epilogue none = {};
+    const moe_int8_epilogue &e = epilogue ? *epilogue : none;
+    if (e.activation < MOE_ACT_NONE || e.activation > MOE_ACT_SIGMOID)
+        return fail(MOE_INT4_EINVAL, "activation %d is none of MOE_ACT_*", e.activation);
+    if (a.places == 0) return MOE_INT4_OK;
+    if ((rc = check_ptrs({{"x", x}, {"w_packed", w_packed}, {"w_scales", w_scales}}))) return rc;
+    const int64_t matrices = (int64_t)a.experts * a.N;
+    const Rows rx{"x", x, MOE_TYPE_BF16, x_stride, a.x_rows, a.K};
+    const Rows ro{"out", out, out_type, out_stride, a.out_rows, a.N};
+    const Rows rb{"bias", e.bias, e.bias_type, 0, 1, matrices};
+    const Rows rr{"residual", e.residual, e.residual_type, e.residual_stride, a.out_rows, a.N};
+    const Rows rp{"w_packed", w_packed, MOE_TYPE_F32, 0, 1, matrices * (a.K / 8)};
+    const Rows rs{"w_scales", w_scales, MOE_TYPE_BF16, 0, 1, matrices * (a.K / a.G)};
+    // the tables hold 4-byte words throughout: the fp32 type stands for all
+    const Rows t_off{"offsets", a.offsets, MOE_TYPE_F32, 0, 1, a.experts + 1};
+    const Rows t_gat{"gather", a.gather, MOE_TYPE_F32, 0, 1, a.places};
+    const Rows t_sca{"scatter", a.scatter, MOE_TYPE_F32, 0, 1, a.places};
+    const Rows t_wgt{"row_weights", a.row_weights, MOE_TYPE_F32, 0, 1, a.out_rows};
+    if ((rc = check_rows(rx)) || (rc = check_rows(ro))) return rc;
+    if (a.x_rows > 1 && x_stride % 8)
+        return fail(MOE_INT4_EALIGN, "x: stride %lld is not a multiple of 8", (long long)x_stride);
+    if ((e.bias && (rc = check_rows(rb))) || (e.residual && (rc = check_rows(rr)))) return rc;
+    for (const Rows *t : {&t_off, &t_gat, &t_sca, &t_wgt})
+        if (t->p && (rc = check_rows(*t))) return rc;
+    const char *which = "";
+    if (overlaps_any(ro, {rx, rp, rs, rb, t_off, t_gat, t_sca, t_wgt}, &which))
+        return fail(MOE_INT4_EINVAL, "out overlaps %s", which);
+    if (e.residual && !same_rows(rr, ro) && may_overlap(rr, ro))
+        return fail(MOE_INT4_EINVAL, "out overlaps residual without being the same rows");
+    const size_t need = int4_workspace(a);
+    if (need) {
+        if (!workspace) return fail(MOE_INT4_EINVAL, "workspace is NULL (%zu bytes needed)", need);
+        if (!aligned16(workspace)) return fail(MOE_INT4_EALIGN, "workspace is not 16-byte aligned");
+        if (workspace_bytes < need)
+            return fail(MOE_INT4_EWORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+        const Rows rw{"workspace", workspace, MOE_TYPE_F32, 0, 1, (int64_t)(need / 4)};
+        if (overlaps_any(rw, {ro, rx, rp, rs, rb, rr, t_off, t_gat, t_sca, t_wgt}, &which))
+            return fail(MOE_INT4_EINVAL, "workspace overlaps %s", which);
+    }
+    if ((rc = check_device()) || (rc = check_stream(st))) return rc;
+    a.x = x;
+    a.x_stride = a.x_rows > 1 ? (size_t)x_stride : 0;
+    a.wq = w_packed;
+    a.ws = w_scales;
+    const bool one = a.out_rows <= 1;
+    const bool vec = a.N % 4 == 0 && rows_aligned(ro, 4) && (!e.bias || rows_aligned(rb, 4)) &&
+                     (!e.residual || rows_aligned(rr, 4));
+    a.e = Int8Epilogue{e.bias, e.residual, out, a.x_stride, one ? 0 : (size_t)e.residual_stride,
+                       one ? 0 : (size_t)out_stride, e.bias_type, e.residual_type, out_type, e.activation, vec};
+    return launched(launch_int4_linear(a, workspace, st), "int4 linear");
+}
+
+int32_t moe_int4_linear_workspace_bytes(int32_t tokens, int32_t n, int32_t k, int32_t group, size_t *bytes)
+{
+    g_error.clear();
+    Int4Args a;
+    int32_t rc = int4_sizes(nullptr, tokens, n, k, group, &a);
+    if (rc) return rc;
+    if (!bytes) return fail(MOE_INT4_EINVAL, "bytes is NULL");
+    *bytes = int4_workspace(a);
+    return MOE_INT4_OK;
+}
+
+int32_t moe_int4_linear(const uint16_t *x, int64_t x_stride, const int32_t *w_packed, const uint16_t *w_scales,
+                        int32_t tokens, int32_t n, int32_t k, int32_t group, const moe_int8_epilogue *epilogue,
+                        void *out, int32_t out_type, int64_t out_stride, void *workspace, size_t workspace_bytes,
+                        void *hip_stream)
+{
+    g_error.clear();
+    Int4Args a;
+    int32_t rc = int4_sizes(nullptr, tokens, n, k, group, &a);
+    if (rc) return rc;
+    return int4_call(a, x, x_stride, w_packed, w_scales, epilogue, out, out_type, out_stride, workspace,
+                     workspace_bytes, (hipStream_t)hip_stream);
+}
+
+int32_t moe_int4_grouped_linear_workspace_bytes(const moe_int4_groups *groups, int32_t n, int32_t k, int32_t group,
+                                                size_t *bytes)
+{
+    g_error.clear();
+    if (!groups) return fail(MOE_INT4_EINVAL, "groups is NULL");
+    Int4Args a;
+    int32_t rc = int4_sizes(groups, 0, n, k, group, &a);
+    if (rc) return rc;
+    if (!bytes) return fail(MOE_INT4_EINVAL, "bytes is NULL");
+    *bytes = int4_workspace(a);
+    return MOE_INT4_OK;
+}
+
+int32_t moe_int4_grouped_linear(const uint16_t *x, int64_t x_stride, const int32_t *w_packed,
+                                const uint16_t *w_scales, const moe_int4_groups *groups, int32_t n, int32_t k,
+                                int32_t group, const moe_int8_epilogue *epilogue, void *out, int32_t out_type,
+                                int64_t out_stride, void *workspace, size_t workspace_bytes, void *hip_stream)
+{
+    g_error.clear();
+    if (!groups) return fail(MOE_INT4_EINVAL, "groups is NULL");
+    Int4Args a;
+    int32_t rc = int4_sizes(groups, 0, n, k, group, &a);
+    if (rc) return rc;
+    if (a.places > 0 && !a.offsets) return fail(MOE_INT4_EINVAL, "offsets is NULL");
+    return int4_call(a, x, x_stride, w_packed, w_scales, epilogue, out, out_type, out_stride, workspace,
+                     workspace_bytes, (hipStream_t)hip_stream);
+}
+
+// ---- verification of drafted tokens ----
+
+static int32_t check_verify_sizes(int32_t seqs, int32_t width, int32_t vocab)
+{
+    if (seqs < 0 || seqs > (1 << 16)) return fail(MOE_INT4_EINVAL, "seqs=%d outside [0, 65536]", seqs);
+    if (width < 0 || width > 64) return fail(MOE_INT4_EINVAL, "width=%d outside [0, 64]", width);
+    if (vocab < 1 || vocab > (1 << 24)) return fail(MOE_INT4_EINVAL, "vocab=%d outside [1, 16777216]", vocab);
+    // fewer than 2^24 slabs of 8192: fewer than 2^32 threads in one launch
+    const int64_t rows = (int64_t)seqs * (2 * width + 1);
+    if (rows > (1 << 20) || rows * vocab > ((int64_t)1 << 36))
+        return fail(MOE_INT4_EINVAL, "seqs * (2 width + 1) = %lld must be at most 2^20, with vocab at most 2^36",
+                    (long long)rows);
+    return MOE_INT4_OK;
+}
+
+int32_t moe_int4_verify_drafts_workspace_bytes(int32_t seqs, int32_t width, int32_t vocab, size_t *bytes)
+{
+    g_error.clear();
+    int32_t rc = check_verify_sizes(seqs, width, vocab);
+    if (rc) return rc;
+    if (!bytes) return fail(MOE_INT4_EINVAL, "bytes is NULL");
+    *bytes = verify_workspace(seqs, width, vocab);
+    return MOE_INT4_OK;
+}
+
+int32_t moe_int4_verify_drafts(const moe_int4_drafts *drafts, int32_t *accepted, int32_t *out_tokens,
+                               void *workspace, size_t workspace_bytes, void *hip_stream)
+{
+    g_error.clear();
+    if (!drafts) return fail(MOE_INT4_EINVAL, "drafts is NULL");
+    const moe_int4_drafts &d = *drafts;
+    int32_t rc = check_verify_sizes(d.seqs, d.width, d.vocab);
+    if (rc) return rc;
+    if (d.seqs == 0) return MOE_INT4_OK;
+    const int64_t seqs = d.seqs, width = d.width;
+    // 4-byte words throughout, but for the logits
+    const Rows rt{"target", d.target, d.target_type, d.target_stride, seqs * (width + 1), d.vocab};
+    const Rows rd{"draft", d.draft, d.draft_type, d.draft_stride, seqs * width, d.vocab};
+    const Rows rk{"tokens", d.tokens, MOE_TYPE_F32, 0, 1, seqs * width};
+    const Rows rl{"lengths", d.lengths, MOE_TYPE_F32, 0, 1, seqs};
+    const Rows rc_{"coins", d.coins, MOE_TYPE_F32, 0, 1, seqs * width};
+    const Rows rk2{"picks", d.picks, MOE_TYPE_F32, 0, 1, seqs};
+    const Rows rm{"temperature", d.temperature, MOE_TYPE_F32, 0, 1, seqs};
+    const Rows ra{"accepted", accepted, MOE_TYPE_F32, 0, 1, seqs};
+    const Rows ro{"out_tokens", out_tokens, MOE_TYPE_F32, 0, 1, seqs * (width + 1)};
+    for (const Rows *t : {&rt, &rk2, &ra, &ro})
+        if ((rc = check_rows(*t))) return rc;
+    for (const Rows *t : {&rk, &rc_})
+        if (width && (rc = check_rows(*t))) return rc;
+    for (const Rows *t : {&rl, &rm})
+        if (t->p && (rc = check_rows(*t))) return rc;
+    if (d.draft && width && (rc = check_rows(rd))) return rc;
+    const char *which = "";
+    if (overlaps_any(ra, {ro, rt, rd, rk, rl, rc_, rk2, rm}, &which))
+        return fail(MOE_INT4_EINVAL, "accepted overlaps %s", which);
+    if (overlaps_any(ro, {rt, rd, rk, rl, rc_, rk2, rm}, &which))
+        return fail(MOE_INT4_EINVAL, "out_tokens overlaps %s", which);
+    const size_t need = verify_workspace(d.seqs, d.width, d.vocab);
+    if (!workspace) return fail(MOE_INT4_EINVAL, "workspace is NULL (%zu bytes needed)", need);
+    if (!aligned16(workspace)) return fail(MOE_INT4_EALIGN, "workspace is not 16-byte aligned");
+    if (workspace_bytes < need)
+        return fail(MOE_INT4_EWORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+    const Rows rw{"workspace", workspace, MOE_TYPE_F32, 0, 1, (int64_t)(need / 4)};
+    if (overlaps_any(rw, {ra, ro, rt, rd, rk, rl, rc_, rk2, rm}, &which))
+        return fail(MOE_INT4_EINVAL, "workspace overlaps %s", which);
+    if ((rc = check_device()) || (rc = check_stream((hipStream_t)hip_stream))) return rc;
+    VerifyArgs a{};
+    a.target = d.target;
+    a.draft = width ? d.draft : nullptr;
+    a.target_stride = rt.rows > 1 ? (size_t)d.target_stride : 0;
+    a.draft_stride = rd.rows > 1 ? (size_t)d.draft_stride : 0;
+    a.target_type = d.target_type;
+    a.draft_type = d.draft_type;
+    a.tokens = d.tokens;
+    a.lengths = d.lengths;
+    a.coins = d.coins;
+    a.picks = d.picks;
+    a.temperature = d.temperature;
+    a.seqs = d.seqs;
+    a.width = d.width;
+    a.vocab = d.vocab;
+    a.accepted = accepted;
+    a.out_tokens = out_tokens;
+    return launched(launch_verify(a, workspace, (hipStream_t)hip_stream), "verify drafts");
+}
+
 }  // extern "C"

@@ -625,4 +625,38 @@ struct LogitsArgs {
 };
 hipError_t launch_logits(const LogitsArgs &a, int in_type, int out_type, hipStream_t st);
 
+// ---------------------------------------------------------------------------
+// INT4 linear layer and products grouped by expert (int4_linear.hip)
+// ---------------------------------------------------------------------------
+struct Int4Args {
+    const uint16_t *x;
+    size_t x_stride;         // elements; 0 with one row
+    const int32_t *wq;       // [experts][N][K / 8]
+    const uint16_t *ws;      // [experts][N][K / G]
+    int N, K, G;
+    int places;              // rows of the sorted order (tokens, without tables)
+    int experts, x_rows, out_rows, gather_div;
+    const int32_t *offsets;  // null: every place belongs to the one matrix, and places are rows
+    const int32_t *gather, *scatter;
+    const float *row_weights;
+    Int8Epilogue e;          // its bias [experts][N]
+};
+size_t int4_workspace(const Int4Args &a);
+hipError_t launch_int4_linear(const Int4Args &a, void *workspace, hipStream_t st);
+
+// ---------------------------------------------------------------------------
+// Verification of drafted tokens (verify.hip)
+// ---------------------------------------------------------------------------
+struct VerifyArgs {
+    const void *target, *draft;
+    size_t target_stride, draft_stride;   // elements
+    int target_type, draft_type;
+    const int32_t *tokens, *lengths;
+    const float *coins, *picks, *temperature;
+    int seqs, width, vocab;
+    int32_t *accepted, *out_tokens;
+};
+size_t verify_workspace(int seqs, int width, int vocab);
+hipError_t launch_verify(const VerifyArgs &a, void *workspace, hipStream_t st);
+
 }  // namespace moe

@@ -188,3 +188,152 @@ class LogitsRules:
             out = torch.empty(logits.shape, dtype=out_dtype, device=logits.device)
         B.moe_int4_logits_process(logits, self._c, out)
         return out
+
+
+class Int4Linear:
+    """A resident INT4 W4A16 linear layer (a draft head's projection, weights
+    as moe_int4_quantize writes them) with its bias and activation: packed
+    int32 [n, k/8], scales bf16 [n, k/group], bias [n] in bf16, fp16 or fp32."""
+
+    def __init__(self, packed: torch.Tensor, scales: torch.Tensor, group: int = 128,
+                 bias: torch.Tensor | None = None, activation: str = "none"):
+        if packed.dim() != 2:
+            raise ValueError(f"packed is {packed.dtype} {tuple(packed.shape)}, expected contiguous int32 [n, k/8]")
+        self.n, self.k, self.group = int(packed.shape[0]), 8 * int(packed.shape[1]), int(group)
+        B.check_int4_weights(packed, scales, (self.n,), self.k, self.group)
+        if activation not in B.ACTIVATIONS:
+            raise ValueError(f"activation {activation!r} is none of {', '.join(B.ACTIVATIONS)}")
+        self.packed, self.scales, self.bias, self.activation = packed, scales, bias, activation
+        self._need = {}
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+        """residual + act(x W^T + bias) on torch's current stream of x's
+        device; x bf16 [tokens, k].  out may be the residual."""
+        tokens = x.shape[0]
+        if out is None:
+            out = torch.empty(tokens, self.n, dtype=out_dtype, device=x.device)
+        need = self._need.get(tokens)
+        if need is None:
+            need = self._need[tokens] = B.moe_int4_linear_workspace_bytes(tokens, self.n, self.k, self.group)
+        # taken anew for every call, as in Int8Linear
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        B.int4_linear(x, self.packed, self.scales, tokens, self.n, self.k, self.group, out, self.bias, residual,
+                      self.activation, workspace)
+        return out
+
+
+class Int4GroupedLinear:
+    """One product of resident INT4 experts over rows grouped by expert, as
+    MoeInt4Layer.route answers them: packed int32 [experts, n, k/8], scales
+    bf16 [experts, n, k/group], bias [experts, n] in bf16, fp16 or fp32."""
+
+    def __init__(self, packed: torch.Tensor, scales: torch.Tensor, group: int = 128,
+                 bias: torch.Tensor | None = None, activation: str = "none"):
+        if packed.dim() != 3:
+            raise ValueError(f"packed is {packed.dtype} {tuple(packed.shape)}, expected contiguous int32 "
+                             "[experts, n, k/8]")
+        self.experts, self.n, self.k = int(packed.shape[0]), int(packed.shape[1]), 8 * int(packed.shape[2])
+        self.group = int(group)
+        B.check_int4_weights(packed, scales, (self.experts, self.n), self.k, self.group)
+        if activation not in B.ACTIVATIONS:
+            raise ValueError(f"activation {activation!r} is none of {', '.join(B.ACTIVATIONS)}")
+        self.packed, self.scales, self.bias, self.activation = packed, scales, bias, activation
+        self._need = {}
+
+    def forward(self, x: torch.Tensor, offsets: torch.Tensor, gather: torch.Tensor | None = None,
+                gather_div: int = 1, scatter: torch.Tensor | None = None, row_weights: torch.Tensor | None = None,
+                residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+        """residual + row_weights act(x W_e^T + bias_e) on torch's current
+        stream of x's device; x bf16 [rows, k].  offsets int32 [experts + 1];
+        place p of expert e (offsets[e] <= p < offsets[e + 1]) reads row
+        gather[p] // gather_div of x and writes row scatter[p] of out (row p
+        without the table), scaled by that row's entry of row_weights.  With r
+        = MoeInt4Layer.route(x): a gate/up product takes gather =
+        r["sorted_slots"] and gather_div = top_k, a down product scatter =
+        r["sorted_slots"] and row_weights = r["weights"].  A new out has as
+        many rows as there are places; rows that no place writes hold zeros
+        where it is made here, and stay as they were in a given one."""
+        if offsets.shape != (self.experts + 1,):
+            raise ValueError(f"offsets is {tuple(offsets.shape)}, expected ({self.experts + 1},)")
+        table = gather if gather is not None else scatter
+        places = x.shape[0] if table is None else table.numel()
+        if out is None:
+            out = torch.zeros(places, self.n, dtype=out_dtype, device=x.device)
+        c = B.make_groups(x.shape[0], out.shape[0], places, offsets, gather, gather_div, scatter, row_weights)
+        index = B.device_index(x, "x")
+        for name, t in (("offsets", offsets), ("gather", gather), ("scatter", scatter), ("row_weights", row_weights)):
+            if t is not None:
+                B.device_index(t, name, index)
+        key = (places, c.x_rows, gather is None)
+        need = self._need.get(key)
+        if need is None:
+            need = self._need[key] = B.moe_int4_grouped_linear_workspace_bytes(c, self.n, self.k, self.group)
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        B.int4_grouped_linear(x, self.packed, self.scales, c, self.n, self.k, self.group, out, self.bias, residual,
+                              self.activation, workspace)
+        return out
+
+
+class DraftVerifier:
+    """Verifies the drafted tokens of a batch against the target's logits, and
+    draws each sequence's next token.  temperature float32 [seqs] is the table
+    that LogitsRules takes: sequences without one above zero are greedy."""
+
+    def __init__(self, vocab: int, temperature: torch.Tensor | None = None):
+        self.vocab = int(vocab)
+        if temperature is not None and (temperature.dtype != torch.float32 or temperature.dim() != 1
+                                        or not temperature.is_contiguous()):
+            raise ValueError(f"temperature is {temperature.dtype} {tuple(temperature.shape)}, expected contiguous "
+                             "float32 [seqs]")
+        self.temperature = temperature
+        self._need = {}
+
+    def verify(self, target: torch.Tensor, drafted: torch.Tensor, coins: torch.Tensor, picks: torch.Tensor,
+               draft: torch.Tensor | None = None, lengths: torch.Tensor | None = None,
+               tokens: torch.Tensor | None = None, accepted: torch.Tensor | None = None) -> tuple:
+        """target [seqs * (width + 1), vocab] and draft [seqs * width, vocab]
+        (None: drafts found by lookup) logits in bf16, fp16 or fp32, as
+        LogitsRules leaves them; drafted int32 [seqs, width], of which lengths
+        int32 [seqs] count; coins float32 [seqs, width] and picks float32
+        [seqs] random numbers in [0, 1).  Answers (tokens int32 [seqs, width +
+        1]: the accepted drafts, the next token, -1 behind it; accepted int32
+        [seqs])."""
+        if drafted.dim() != 2:
+            raise ValueError(f"drafted is {tuple(drafted.shape)}, expected [seqs, width]")
+        seqs, width = drafted.shape
+        if self.temperature is not None and self.temperature.shape[0] < seqs:
+            raise ValueError(f"temperature has {self.temperature.shape[0]} sequences, drafted {seqs}")
+        index = B.device_index(target, "target")
+        c = B.MoeDrafts()
+        for name, t, dtype, shape in (("tokens", drafted, torch.int32, (seqs, width)),
+                                      ("lengths", lengths, torch.int32, (seqs,)),
+                                      ("coins", coins, torch.float32, (seqs, width)),
+                                      ("picks", picks, torch.float32, (seqs,))):
+            if t is None:
+                continue
+            if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+                raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected contiguous {dtype} {shape}")
+            B.device_index(t, name, index)
+            setattr(c, name, t.data_ptr())
+        if self.temperature is not None:
+            B.device_index(self.temperature, "temperature", index)
+            c.temperature = self.temperature.data_ptr()
+        c.target_stride = B.row_stride(target, "target", seqs * (width + 1), self.vocab)
+        c.target, c.target_type = target.data_ptr(), B.type_code(target.dtype)
+        if draft is not None:
+            c.draft_stride = B.row_stride(draft, "draft", seqs * width, self.vocab)
+            c.draft, c.draft_type = draft.data_ptr(), B.type_code(draft.dtype)
+            B.device_index(draft, "draft", index)
+        c.seqs, c.width, c.vocab = seqs, width, self.vocab
+        if tokens is None:
+            tokens = torch.empty(seqs, width + 1, dtype=torch.int32, device=target.device)
+        if accepted is None:
+            accepted = torch.empty(seqs, dtype=torch.int32, device=target.device)
+        need = self._need.get((seqs, width))
+        if need is None:
+            need = self._need[seqs, width] = B.moe_int4_verify_drafts_workspace_bytes(seqs, width, self.vocab)
+        workspace = torch.empty(need, dtype=torch.uint8, device=target.device)
+        B.moe_int4_verify_drafts(c, accepted, tokens, workspace)
+        return tokens, accepted
