@@ -414,8 +414,8 @@ int32_t moe_int4_logits_process(const void *logits, int32_t logits_type, int64_t
  * may overflow on the way, and a token with an infinity or a NaN in x has NaN
  * in all its own outputs (before activation and residual), and in no others.
  * group is 64 or 128, k a multiple of it (at most 65536), n in [1, 2^24],
- * tokens in [0, 2^20] with tokens * n and tokens * k below 2^31; tokens = 0 is
- * a no-op.  Strides, alignment, overlaps, workspace and streams as in
+ * tokens in [0, 2^20] with tokens * n and (tokens + 1) * (k rounded up to a
+ * multiple of 128) below 2^31; tokens = 0 is a no-op.  Strides, alignment, overlaps, workspace and streams as in
  * moe_int8_linear_fused.  The result does not depend on timing. */
 int32_t moe_int4_linear_workspace_bytes(int32_t tokens, int32_t n, int32_t k, int32_t group,
                                         size_t *bytes);
@@ -461,8 +461,10 @@ typedef struct moe_int4_groups {
  *             w_scales bf16 [experts][n][k/group]
  *   out       [out_rows][n] of out_type
  *   epilogue  may be NULL; its bias is [experts][n], its residual [out_rows][n]
- * experts in [1, 1024], places, x_rows and out_rows in [0, 2^20], each times n
- * (x_rows: times k) below 2^31; places = 0 is a no-op.  Without gather x has
+ * experts in [1, 1024]; places, x_rows and out_rows in [0, 2^20]; places * n,
+ * out_rows * n, x_rows * k and (places + 1) * (k rounded up to a multiple of
+ * 128) below 2^31, with gather x_rows * x_stride too; min(experts, places) *
+ * n below 2^29; places = 0 is a no-op.  Without gather x has
  * at least places rows, without scatter so has out; a residual that is out
  * itself needs scatter to name no row twice.  Otherwise as moe_int4_linear. */
 int32_t moe_int4_grouped_linear_workspace_bytes(const moe_int4_groups *groups, int32_t n,

@@ -820,10 +820,10 @@ static int32_t check_int4_matrix(int32_t n, int32_t k, int32_t group)
     return MOE_INT4_OK;
 }
 
-static int32_t check_int4_rows(const char *name, int32_t rows, int32_t cols)
+static int32_t check_int4_rows(const char *name, int32_t rows, int32_t cols, int32_t pad = 0)
 {
     if (rows < 0 || rows > (1 << 20)) return fail(MOE_INT4_EINVAL, "%s=%d outside [0, 1048576]", name, rows);
-    if ((long long)rows * cols >= (1LL << 31))
+    if ((long long)(rows + pad) * cols >= (1LL << 31))
         return fail(MOE_INT4_EINVAL, "%s times the row's length must stay below 2^31", name);
     return MOE_INT4_OK;
 }
@@ -838,16 +838,22 @@ static int32_t int4_sizes(const moe_int4_groups *g, int32_t tokens, int32_t n, i
     a->K = k;
     a->G = group;
     a->experts = a->gather_div = 1;
+    // the copy of x in the workspace has whole stages of 128 inputs and a row of
+    // zeros, and its bytes are counted in 32 bits
+    const int32_t kp = (k + 127) / 128 * 128;
     if (!g) {
-        if ((rc = check_int4_rows("tokens", tokens, n)) || (rc = check_int4_rows("tokens", tokens, k))) return rc;
+        if ((rc = check_int4_rows("tokens", tokens, n)) || (rc = check_int4_rows("tokens", tokens, kp, 1))) return rc;
         a->places = a->x_rows = a->out_rows = tokens;
         return MOE_INT4_OK;
     }
     if (g->experts < 1 || g->experts > kMaxExperts)
         return fail(MOE_INT4_EINVAL, "experts=%d outside [1, %d]", g->experts, kMaxExperts);
     if ((rc = check_int4_rows("places", g->places, n)) || (rc = check_int4_rows("out_rows", g->out_rows, n)) ||
-        (rc = check_int4_rows("x_rows", g->x_rows, k)) || (rc = check_int4_rows("places", g->places, k)))
+        (rc = check_int4_rows("x_rows", g->x_rows, k)) || (rc = check_int4_rows("places", g->places, kp, 1)))
         return rc;
+    // fewer than 2^32 threads in one launch: a workgroup takes 16 rows of an expert and 64 columns
+    if ((long long)(g->experts < g->places ? g->experts : g->places) * n >= (1LL << 29))
+        return fail(MOE_INT4_EINVAL, "min(experts, places) * n must stay below 2^29");
     if (g->gather && g->gather_div < 1) return fail(MOE_INT4_EINVAL, "gather_div=%d must be positive", g->gather_div);
     if (g->places > 0 && g->x_rows < (g->gather ? 1 : g->places))
         return fail(MOE_INT4_EINVAL, "x_rows=%d, %d places need %d", g->x_rows, g->places, g->gather ? 1 : g->places);
@@ -891,6 +897,8 @@ static int32_t int4_call(Int4Args &a, const uint16_t *x, int64_t x_stride, const
     if ((rc = check_rows(rx)) || (rc = check_rows(ro))) return rc;
     if (a.x_rows > 1 && x_stride % 8)
         return fail(MOE_INT4_EALIGN, "x: stride %lld is not a multiple of 8", (long long)x_stride);
+    if (a.gather && a.x_rows > 1 && a.x_rows * x_stride >= ((int64_t)1 << 31))   // bytes counted in 32 bits
+        return fail(MOE_INT4_EINVAL, "x: with gather, x_rows * stride must stay below 2^31");
     if ((e.bias && (rc = check_rows(rb))) || (e.residual && (rc = check_rows(rr)))) return rc;
     for (const Rows *t : {&t_off, &t_gat, &t_sca, &t_wgt})
         if (t->p && (rc = check_rows(*t))) return rc;
