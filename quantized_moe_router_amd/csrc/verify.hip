@@ -2,19 +2,31 @@
 // by given random numbers, and the next token from what the target has over the
 // draft.
 //
-// Three launches over slabs of the vocabulary: each slab's largest logit, its
-// first place and the sum of exponentials relative to it, for all rows; each
-// sequence's decision, and by slabs the mass of its next token's distribution;
-// the slab and the token that the pick falls on.  Probabilities and sums are in
-// 64 bits: among 10^5 tokens a pick falls within fp32's error of some border
-// about once in a hundred.
+// Three launches over slabs of 8192 tokens of the vocabulary, each of a
+// workgroup whose threads hold their logits in registers:
+//   stats  each slab's largest logit, its first place (greedy sequences) and
+//          the sum of exponentials relative to it, for all rows that count;
+//   mass   each sequence's decision, from its rows' slabs; where a draft was
+//          refused, the mass of max(0, p - q) in each 256 tokens and slab;
+//   pick   the slab, the 256 tokens and the token that the pick falls on.
+// Behind the last draft the token comes from p itself, whose slabs' masses the
+// first launch has left, so the second has nothing to do for such a sequence
+// and is left out where there are no drafts at all.
+//
+// Probabilities and sums are in 64 bits: among 10^5 tokens a pick falls within
+// fp32's error of some border about once in a hundred.  The vector ALU has half
+// its fp32 rate for them, and the first launch stays bound by the rows' bytes.
 #include "common.h"
 
 namespace moe {
 
 namespace {
 
-constexpr int kSlab = 8192, kThreads = 256;
+constexpr int kSlab = 8192, kThreads = 256, kWaves = kThreads / 64;
+constexpr int kTurns = kSlab / (4 * kThreads);   // of four tokens a thread
+constexpr int kChunk = 256;                      // tokens of a wave's turn
+constexpr int kChunks = kSlab / kChunk;
+constexpr int kMostDrafts = 64;                  // a lane each
 
 // What a slab of a row leaves: its largest logit (-infinity: none) and the first
 // place of it, and the sum of exp(l - largest).
@@ -24,12 +36,36 @@ struct Part {
     int32_t at;
 };
 
-// exp(l - top), with +infinities sharing the probability.
-__device__ __forceinline__ double term(float l, double top)
+// e^d for d <= 0, within 2^-47 of it: 2^k e^r with |r| <= ln 2 / 2, e^r by its
+// Taylor sum up to r^11.  Far below, and for a NaN, 0.
+__device__ __forceinline__ double exp_below(double d)
 {
-    if (!(l > -INFINITY)) return 0.0;   // NaN too
-    const double d = (double)l - top;
-    return (double)l == top ? 1.0 : exp(d);
+    d = fmax(d, -2000.0);   // of a NaN, too, the other one
+    const double k = rint(d * 1.4426950408889634074);
+    // ln 2 as a double with 32 bits, times k exact, and the rest of it
+    double r = fma(k, -0x1.62e42fefp-1, d);
+    r = fma(k, -0x1.473de6af278edp-34, r);
+    double y = 1.0 / 39916800;
+    y = fma(y, r, 1.0 / 3628800);
+    y = fma(y, r, 1.0 / 362880);
+    y = fma(y, r, 1.0 / 40320);
+    y = fma(y, r, 1.0 / 5040);
+    y = fma(y, r, 1.0 / 720);
+    y = fma(y, r, 1.0 / 120);
+    y = fma(y, r, 1.0 / 24);
+    y = fma(y, r, 1.0 / 6);
+    y = fma(y, r, 0.5);
+    y = fma(y, r, 1.0);
+    y = fma(y, r, 1.0);
+    return ldexp(y, (int)k);
+}
+
+// exp(l - top), top the largest of its row or slab; +infinities share the
+// probability; -infinity and NaN have none.
+__device__ __forceinline__ double term(float l, float top)
+{
+    if (top == INFINITY) return l == INFINITY ? 1.0 : 0.0;
+    return exp_below((double)l - (double)top);
 }
 
 __device__ __forceinline__ void larger(float &top, int &at, float other, int place)
@@ -40,185 +76,412 @@ __device__ __forceinline__ void larger(float &top, int &at, float other, int pla
     }
 }
 
-// Sum over the workgroup, in a fixed order.
-__device__ __forceinline__ double block_sum(double v, double *s)
+__device__ __forceinline__ double wave_sum64(double v)
 {
 #pragma unroll
     for (int off = 32; off; off >>= 1) v += __shfl_xor(v, off, 64);
+    return v;
+}
+
+// The sums of this thread and of those before it in the workgroup, in a fixed
+// order; total: of all.
+__device__ __forceinline__ double block_scan(double v, double *s, double &total)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const double o = __shfl_up(v, off, 64);
+        if (lane >= off) v += o;
+    }
+    __syncthreads();
+    if (lane == 63) s[wave] = v;
+    __syncthreads();
+    double base = 0.0;
+    total = 0.0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) base += s[w];
+        total += s[w];
+    }
+    return base + v;
+}
+
+// The smallest of a workgroup's ints.
+__device__ __forceinline__ int block_min(int v, int *s)
+{
+#pragma unroll
+    for (int off = 32; off; off >>= 1) v = min(v, __shfl_xor(v, off, 64));
     __syncthreads();
     if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = 0.0;
-    for (int w = 0; w < kThreads / 64; ++w) v += s[w];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) v = min(v, s[w]);
     return v;
+}
+
+// A row of logits.
+struct Row {
+    const char *p;
+    int type;
+};
+__device__ __forceinline__ Row target_row(const VerifyArgs &a, int seq, int i)
+{
+    return {static_cast<const char *>(a.target) + ((size_t)seq * (a.width + 1) + i) * a.target_stride * type_bytes(a.target_type),
+            a.target_type};
+}
+__device__ __forceinline__ Row draft_row(const VerifyArgs &a, int seq, int i)
+{
+    return {static_cast<const char *>(a.draft) + ((size_t)seq * a.width + i) * a.draft_stride * type_bytes(a.draft_type),
+            a.draft_type};
+}
+
+// This thread's logits of a slab: four consecutive ones a turn, -infinity
+// behind the vocabulary.  All loads are issued before any is used.
+template <int TYPE>
+__device__ __forceinline__ void load_slab_as(const char *row, int v0, int vocab, float (&l)[kTurns][4])
+{
+    constexpr int kBytes = TYPE == kF32 ? 4 : 2;
+    const int v = v0 + 4 * threadIdx.x;
+    if ((uintptr_t)row % (4 * kBytes) == 0 && v0 + kSlab <= vocab) {
+        uint32_t w[kTurns][kBytes];
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+            const void *at = row + (size_t)(v + 4 * kThreads * i) * kBytes;
+            if constexpr (TYPE == kF32) {
+                const uint4 q = *static_cast<const uint4 *>(at);
+                w[i][0] = q.x, w[i][1] = q.y, w[i][2] = q.z, w[i][3] = q.w;
+            } else {
+                const uint2 q = *static_cast<const uint2 *>(at);
+                w[i][0] = q.x, w[i][1] = q.y;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (TYPE == kF32) l[i][j] = __uint_as_float(w[i][j]);
+                else if constexpr (TYPE == kBf16) l[i][j] = j & 1 ? bf16_hi(w[i][j >> 1]) : bf16_lo(w[i][j >> 1]);
+                else l[i][j] = (float)__builtin_bit_cast(f16x2_t, w[i][j >> 1])[j & 1];
+            }
+        return;
+    }
+    uint32_t w[kTurns][4];
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int at = min(v + 4 * kThreads * i + j, vocab - 1);
+            w[i][j] = TYPE == kF32 ? reinterpret_cast<const uint32_t *>(row)[at] : reinterpret_cast<const uint16_t *>(row)[at];
+        }
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float f;
+            if (TYPE == kF32) f = __uint_as_float(w[i][j]);
+            else if (TYPE == kBf16) f = __uint_as_float(w[i][j] << 16);
+            else f = (float)__builtin_bit_cast(_Float16, (uint16_t)w[i][j]);
+            l[i][j] = v + 4 * kThreads * i + j < vocab ? f : -INFINITY;
+        }
+}
+
+__device__ __forceinline__ void load_slab(const Row &r, int v0, int vocab, float (&l)[kTurns][4])
+{
+    if (r.type == kF32) load_slab_as<kF32>(r.p, v0, vocab, l);
+    else if (r.type == kBf16) load_slab_as<kBf16>(r.p, v0, vocab, l);
+    else load_slab_as<kF16>(r.p, v0, vocab, l);
+}
+
+__device__ __forceinline__ int drafts_of(const VerifyArgs &a, int seq)
+{
+    return a.lengths ? min(max(a.lengths[seq], 0), a.width) : a.width;
+}
+__device__ __forceinline__ bool greedy(const VerifyArgs &a, int seq)
+{
+    return a.temperature && !(a.temperature[seq] > 0.f);
 }
 
 __global__ __launch_bounds__(kThreads) void verify_stats_kernel(VerifyArgs a, int slabs, Part *parts)
 {
-    __shared__ double s_sum[4];
-    __shared__ float s_top[4];
-    __shared__ int s_at[4];
-    const int row = blockIdx.x / slabs, slab = blockIdx.x - row * slabs;
+    __shared__ double s_sum[kWaves];
+    __shared__ float s_top[kWaves];
+    __shared__ int s_at[kWaves];
+    const int row = blockIdx.x / slabs, slab = blockIdx.x - row * slabs, v0 = slab * kSlab;
     const int targets = a.seqs * (a.width + 1);
     const bool t = row < targets;
-    const char *p = static_cast<const char *>(t ? a.target : a.draft);
-    const int type = t ? a.target_type : a.draft_type;
-    p += (t ? row * a.target_stride : (row - targets) * a.draft_stride) * type_bytes(type);
-    const int v0 = slab * kSlab, v1 = min(a.vocab, v0 + kSlab);
+    const int seq = t ? row / (a.width + 1) : (row - targets) / a.width;
+    const int i = t ? row - seq * (a.width + 1) : row - targets - seq * a.width;
+    const Row r = t ? target_row(a, seq, i) : draft_row(a, seq, i);
+    const int drafts = drafts_of(a, seq);
+    const bool first_only = greedy(a, seq);
+    if (t ? i > drafts : i >= drafts || first_only) return;   // a row that no decision looks at
+    float l[kTurns][4];
+    load_slab(r, v0, a.vocab, l);
+
     float top = -INFINITY;
-    int at = 0x7FFFFFFF;
-    for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
-        const float l = load_typed(p, type, v);
-        if (l > top) top = l, at = v;
-    }
 #pragma unroll
-    for (int off = 32; off; off >>= 1) larger(top, at, __shfl_xor(top, off, 64), __shfl_xor(at, off, 64));
-    if ((threadIdx.x & 63) == 0) s_top[threadIdx.x >> 6] = top, s_at[threadIdx.x >> 6] = at;
+    for (int k = 0; k < kTurns; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = fmaxf(top, l[k][j]);   // passes over a NaN
+#pragma unroll
+    for (int off = 32; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+    if ((threadIdx.x & 63) == 0) s_top[threadIdx.x >> 6] = top;
     __syncthreads();
-    for (int w = 0; w < kThreads / 64; ++w) larger(top, at, s_top[w], s_at[w]);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_top[w]);
+    int at = 0x7FFFFFFF;
     double sum = 0.0;
-    for (int v = v0 + threadIdx.x; v < v1; v += kThreads) sum += term(load_typed(p, type, v), (double)top);
-    sum = block_sum(sum, s_sum);
+    if (first_only) {
+#pragma unroll
+        for (int k = kTurns - 1; k >= 0; --k)
+#pragma unroll
+            for (int j = 3; j >= 0; --j)
+                if (l[k][j] == top) at = v0 + 4 * (int)threadIdx.x + 4 * kThreads * k + j;
+        at = block_min(at, s_at);
+    } else if (top == INFINITY) {
+#pragma unroll
+        for (int k = 0; k < kTurns; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum += l[k][j] == top ? 1.0 : 0.0;
+        block_scan(sum, s_sum, sum);
+    } else if (top > -INFINITY) {
+#pragma unroll
+        for (int k = 0; k < kTurns; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum += exp_below((double)l[k][j] - (double)top);
+        block_scan(sum, s_sum, sum);
+    }
     if (threadIdx.x == 0) parts[(size_t)row * slabs + slab] = Part{sum, top, at};
 }
 
-// A row's largest logit, its place and the sum of its exponentials, from its slabs.
+// A row's largest logit, its place and the sum of its exponentials, from its
+// slabs; by one wave.
 __device__ __forceinline__ Part row_of(const Part *p, int slabs)
 {
+    const int lane = threadIdx.x & 63;
     Part r{0.0, -INFINITY, 0x7FFFFFFF};
-    for (int i = 0; i < slabs; ++i) larger(r.top, r.at, p[i].top, p[i].at);
-    for (int i = 0; i < slabs; ++i)
-        if (p[i].top > -INFINITY) r.sum += p[i].sum * term(p[i].top, (double)r.top);
+    for (int i = lane; i < slabs; i += 64) larger(r.top, r.at, p[i].top, p[i].at);
+#pragma unroll
+    for (int off = 32; off; off >>= 1) larger(r.top, r.at, __shfl_xor(r.top, off, 64), __shfl_xor(r.at, off, 64));
+    if (r.top > -INFINITY)
+        for (int i = lane; i < slabs; i += 64) r.sum += p[i].sum * term(p[i].top, r.top);
+    r.sum = wave_sum64(r.sum);
     return r;
-}
-
-__device__ __forceinline__ double probability(const Part &r, float l)
-{
-    return r.sum > 0.0 ? term(l, (double)r.top) / r.sum : 0.0;
 }
 
 // What a sequence's drafts come to: how many are accepted, and the rows that the
 // next token is drawn from.
 struct Decision {
     int accepted, drafts;
-    bool greedy;
-    Part p, q;
+    bool first_only;   // greedy
+    Part p, q;         // of the row behind the accepted drafts; q.sum 0: nothing is taken off
 };
 
-__device__ __forceinline__ Decision decide(const VerifyArgs &a, const Part *parts, int slabs, int seq)
+__device__ __forceinline__ double probability(const Part &r, float l)
 {
-    Decision d{};
-    d.drafts = a.lengths ? min(max(a.lengths[seq], 0), a.width) : a.width;
-    d.greedy = a.temperature && !(a.temperature[seq] > 0.f);
+    return r.sum > 0.0 ? term(l, r.top) / r.sum : 0.0;
+}
+
+struct DecisionSpace {
+    Part p[kMostDrafts + 1], q[kMostDrafts];
+    int accepted;
+};
+
+// By all threads of a workgroup: a wave takes a row at a time, then a lane each
+// draft.
+__device__ __forceinline__ Decision decide(const VerifyArgs &a, const Part *parts, int slabs, int seq, DecisionSpace &s)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    Decision d;
+    d.drafts = drafts_of(a, seq);
+    d.first_only = greedy(a, seq);
+    const bool have_q = a.draft && !d.first_only;
+    // this lane's draft and its logits
+    int x = -1;
+    float lp = -INFINITY, lq = -INFINITY, coin = 0.f;
+    if (wave == 0 && lane < d.drafts) {
+        x = a.tokens[seq * a.width + lane];
+        coin = a.coins[seq * a.width + lane];
+        if (x >= 0 && x < a.vocab && !d.first_only) {
+            const Row rp = target_row(a, seq, lane);
+            lp = load_typed(rp.p, rp.type, x);
+            if (have_q) {
+                const Row rq = draft_row(a, seq, lane);
+                lq = load_typed(rq.p, rq.type, x);
+            }
+        }
+    }
     const Part *pt = parts + (size_t)seq * (a.width + 1) * slabs;
     const Part *pd = parts + ((size_t)a.seqs * (a.width + 1) + (size_t)seq * a.width) * slabs;
-    for (int n = 0;; ++n) {
-        d.accepted = n;
-        d.p = row_of(pt + (size_t)n * slabs, slabs);
-        if (n == d.drafts) return d;
-        const int x = a.tokens[seq * a.width + n];
-        const bool in = x >= 0 && x < a.vocab;
-        if (d.greedy) {
-            if (!(d.p.top > -INFINITY) || x != d.p.at) return d;
-            continue;
+    const int rows = d.drafts + 1 + (have_q ? d.drafts : 0);
+    for (int i = wave; i < rows; i += kWaves) {
+        const bool t = i <= d.drafts;
+        const Part r = row_of(t ? pt + (size_t)i * slabs : pd + (size_t)(i - d.drafts - 1) * slabs, slabs);
+        if (lane == 0) (t ? s.p[i] : s.q[i - d.drafts - 1]) = r;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        bool good = false;
+        if (lane < d.drafts) {
+            const Part p = s.p[lane];
+            if (d.first_only) {
+                good = p.top > -INFINITY && x == p.at;
+            } else if (x >= 0 && x < a.vocab) {
+                const double qx = a.draft ? probability(s.q[lane], lq) : 1.0;
+                good = (double)coin * qx < probability(p, lp);
+            }
         }
-        double px = 0.0, qx = in ? 1.0 : 0.0;
-        if (in)
-            px = probability(d.p, load_typed(a.target, a.target_type, ((size_t)seq * (a.width + 1) + n) * a.target_stride + x));
+        const uint64_t bad = ~__ballot(good);   // beyond the drafts, too
+        if (lane == 0) s.accepted = bad ? min(d.drafts, __ffsll((unsigned long long)bad) - 1) : d.drafts;
+    }
+    __syncthreads();
+    d.accepted = s.accepted;
+    d.p = s.p[d.accepted];
+    d.q = Part{0.0, -INFINITY, -1};
+    if (d.accepted < d.drafts && !d.first_only) {
         if (a.draft) {
-            d.q = row_of(pd + (size_t)n * slabs, slabs);
-            if (in)
-                qx = probability(d.q, load_typed(a.draft, a.draft_type, ((size_t)seq * a.width + n) * a.draft_stride + x));
+            d.q = s.q[d.accepted];
+        } else {   // all of q at the drafted token
+            const int at = a.tokens[seq * a.width + d.accepted];
+            d.q = Part{at >= 0 && at < a.vocab ? 1.0 : 0.0, -INFINITY, at};
         }
-        if (!((double)a.coins[seq * a.width + n] * qx < px)) return d;
+    }
+    return d;
+}
+
+// p and r = max(0, p - q) of one token.  ip, iq: 1 / sum, or 0.  A quotient is
+// a product with them: an ulp more of 64 bits.  Both products are rounded before
+// the subtraction: with one of them inside a fused step, equal rows would leave
+// the other's rounding error.
+__device__ __forceinline__ double token_r(const VerifyArgs &a, const Decision &d, double ip, double iq, int v, float lp, float lq)
+{
+#pragma clang fp contract(off)
+    const double p = term(lp, d.p.top) * ip;
+    const double q = a.draft ? term(lq, d.q.top) * iq : (v == d.q.at ? iq : 0.0);
+    const double r = p - q;
+    return r > 0.0 ? r : 0.0;
+}
+__device__ __forceinline__ double inverse(double s) { return s > 0.0 ? 1.0 / s : 0.0; }
+
+// The masses of r: chunks[seq][slab][kChunks] and slabs_r[seq][slab].
+__global__ __launch_bounds__(kThreads) void verify_mass_kernel(VerifyArgs a, int slabs, const Part *parts, double *chunks, double *slab_r)
+{
+    __shared__ DecisionSpace s;
+    __shared__ double s_sum[kWaves];
+    const int seq = blockIdx.x / slabs, slab = blockIdx.x - seq * slabs, v0 = slab * kSlab;
+    const Decision d = decide(a, parts, slabs, seq, s);
+    if (d.first_only || !(d.q.sum > 0.0)) return;   // the largest, or p itself
+    float lp[kTurns][4], lq[kTurns][4];
+    load_slab(target_row(a, seq, d.accepted), v0, a.vocab, lp);
+    if (a.draft) load_slab(draft_row(a, seq, d.accepted), v0, a.vocab, lq);
+    const double ip = inverse(d.p.sum), iq = inverse(d.q.sum);
+    double all = 0.0;
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        const int v = v0 + 4 * (int)threadIdx.x + 4 * kThreads * k;
+        double r = 0.0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r += token_r(a, d, ip, iq, v + j, lp[k][j], a.draft ? lq[k][j] : 0.f);
+        r = wave_sum64(r);
+        if ((threadIdx.x & 63) == 0) chunks[((size_t)seq * slabs + slab) * kChunks + k * kWaves + (threadIdx.x >> 6)] = r;
+        all += r;
+    }
+    if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = all;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kWaves; ++w) all += s_sum[w];
+        slab_r[(size_t)seq * slabs + slab] = all;
     }
 }
 
-// r of one token.
-__device__ __forceinline__ double over(const VerifyArgs &a, const Decision &d, int seq, int v, bool rest)
+// The first of `count` masses up to which their sum, with `before`, exceeds
+// `mark`; else the last that is not zero (rounding).  before: becomes the sum of
+// those ahead of it.  By all threads.
+template <class Mass>
+__device__ __forceinline__ int find_mass(int count, Mass mass, double mark, double &before, double *s_sum, int *s_int, double *s_before)
 {
-    const double p = probability(d.p, load_typed(a.target, a.target_type, ((size_t)seq * (a.width + 1) + d.accepted) * a.target_stride + v));
-    if (d.accepted == d.drafts || !rest) return p;
-    double q;
-    if (a.draft)
-        q = probability(d.q, load_typed(a.draft, a.draft_type, ((size_t)seq * a.width + d.accepted) * a.draft_stride + v));
-    else
-        q = v == a.tokens[seq * a.width + d.accepted] ? 1.0 : 0.0;
-    return fmax(p - q, 0.0);
-}
-
-// masses[seq][slab] = {sum of max(0, p - q), sum of p}
-__global__ __launch_bounds__(kThreads) void verify_mass_kernel(VerifyArgs a, int slabs, const Part *parts, double2 *masses)
-{
-    __shared__ double s_sum[4];
-    const int seq = blockIdx.x / slabs, slab = blockIdx.x - seq * slabs;
-    const Decision d = decide(a, parts, slabs, seq);
-    if (d.greedy) return;
-    const int v0 = slab * kSlab, v1 = min(a.vocab, v0 + kSlab);
-    double r = 0.0, p = 0.0;
-    for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
-        r += over(a, d, seq, v, true);
-        p += over(a, d, seq, v, false);
+    int found = 0x7FFFFFFF, last = -1;
+    for (int i0 = 0; i0 < count && found == 0x7FFFFFFF; i0 += kThreads) {
+        const int i = i0 + threadIdx.x;
+        const double m = i < count ? mass(i) : 0.0;
+        double total;
+        const double run = before + block_scan(m, s_sum, total);
+        found = block_min(m > 0.0 && run > mark ? i : 0x7FFFFFFF, s_int);
+        const int l = -block_min(m > 0.0 ? -i : 1, s_int);
+        if (l >= 0) last = l;
+        const int mine = found != 0x7FFFFFFF ? found : l;
+        if (mine == i) *s_before = run - m;
+        __syncthreads();
+        if (found == 0x7FFFFFFF) before += total;
     }
-    r = block_sum(r, s_sum);
-    p = block_sum(p, s_sum);
-    if (threadIdx.x == 0) masses[(size_t)seq * slabs + slab] = make_double2(r, p);
+    if (last >= 0) before = *s_before;
+    __syncthreads();
+    return found != 0x7FFFFFFF ? found : last;
 }
 
-// One workgroup per sequence: the slab of the pick, then its token.
-__global__ __launch_bounds__(kThreads) void verify_pick_kernel(VerifyArgs a, int slabs, const Part *parts, const double2 *masses)
+// One workgroup per sequence.
+__global__ __launch_bounds__(kThreads) void verify_pick_kernel(VerifyArgs a, int slabs, const Part *parts, const double *chunks, const double *slab_r)
 {
-    __shared__ double s_run[kThreads];
+    __shared__ DecisionSpace s;
+    __shared__ double s_sum[kWaves], s_chunk[kChunks], s_before;
+    __shared__ int s_int[kWaves];
     const int seq = blockIdx.x, tid = threadIdx.x;
-    const Decision d = decide(a, parts, slabs, seq);
+    const Decision d = decide(a, parts, slabs, seq, s);
     int token = -1;
-    if (d.greedy) {
+    if (d.first_only) {
         token = d.p.top > -INFINITY ? d.p.at : -1;
     } else if (d.p.sum > 0.0) {
-        const double2 *m = masses + (size_t)seq * slabs;
-        double total = 0.0, all = 0.0;
-        for (int i = 0; i < slabs; ++i) total += m[i].x, all += m[i].y;
-        const bool rest = total > 0.0;
-        if (!rest) total = all;
+        const Part *pt = parts + ((size_t)seq * (a.width + 1) + d.accepted) * slabs;
+        const double *mr = slab_r + (size_t)seq * slabs;
+        bool rest = d.q.sum > 0.0;
+        auto mass = [&](int i) { return rest ? mr[i] : pt[i].sum > 0.0 ? pt[i].sum * term(pt[i].top, d.p.top) : 0.0; };
+        auto sum_of = [&]() {
+            double all = 0.0, total;
+            for (int i = tid; i < slabs; i += kThreads) all += mass(i);
+            block_scan(all, s_sum, total);
+            return total;
+        };
+        double total = sum_of();
+        if (rest && !(total > 0.0)) {   // the draft has all that the target has
+            rest = false;
+            total = sum_of();
+        }
         const double mark = (double)a.picks[seq] * total;
-        // the first slab whose end passes the mark; the last with any mass, where rounding leaves none
-        double before = 0.0, run = 0.0;
-        int slab = 0;
-        for (int i = 0; i < slabs; ++i) {
-            const double w = rest ? m[i].x : m[i].y;
-            if (w > 0.0) {
-                slab = i, before = run;
-                run += w;
-                if (run > mark) break;
+        // (of p the masses are exp(l - top) here, without the division by their sum)
+        const double ip = rest ? inverse(d.p.sum) : 1.0, iq = inverse(d.q.sum);
+        double before = 0.0;
+        const int slab = find_mass(slabs, mass, mark, before, s_sum, s_int, &s_before);
+        const Row rp = target_row(a, seq, d.accepted);
+        if (!rest) {
+            float lp[kTurns][4];
+            load_slab(rp, slab * kSlab, a.vocab, lp);
+#pragma unroll
+            for (int k = 0; k < kTurns; ++k) {
+                double m = 0.0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m += term(lp[k][j], d.p.top);
+                m = wave_sum64(m);
+                if ((tid & 63) == 0) s_chunk[k * kWaves + (tid >> 6)] = m;
             }
+        } else if (tid < kChunks) {
+            s_chunk[tid] = chunks[((size_t)seq * slabs + slab) * kChunks + tid];
         }
-        // 32 consecutive tokens to a thread
-        constexpr int kPer = kSlab / kThreads;
-        const int v0 = slab * kSlab + tid * kPer, v1 = min(a.vocab, v0 + kPer);
-        double mine = 0.0;
-        for (int v = v0; v < v1; ++v) mine += over(a, d, seq, v, rest);
-        s_run[tid] = mine;
         __syncthreads();
-        run = before;
-        for (int i = 0; i < tid; ++i) run += s_run[i];
-        int last = -1;
-        bool found = false;
-        for (int v = v0; v < v1 && !found; ++v) {
-            const double w = over(a, d, seq, v, rest);
-            if (w > 0.0) {
-                run += w;
-                last = v;
-                found = run > mark;
+        const int chunk = find_mass(kChunks, [&](int i) { return s_chunk[i]; }, mark, before, s_sum, s_int, &s_before);
+        const int v0 = slab * kSlab + chunk * kChunk;
+        auto one = [&](int i) {
+            const int v = v0 + i;
+            if (v >= a.vocab) return 0.0;
+            const float lp = load_typed(rp.p, rp.type, v);
+            if (!rest) return term(lp, d.p.top);
+            float lq = 0.f;
+            if (a.draft) {
+                const Row rq = draft_row(a, seq, d.accepted);
+                lq = load_typed(rq.p, rq.type, v);
             }
-        }
-        // the first found; else the slab's last token with any mass
-        __shared__ int s_first, s_last;
-        if (tid == 0) s_first = 0x7FFFFFFF, s_last = -1;
-        __syncthreads();
-        if (found) atomicMin(&s_first, last);
-        if (last >= 0) atomicMax(&s_last, last);
-        __syncthreads();
-        token = s_first != 0x7FFFFFFF ? s_first : s_last;
+            return token_r(a, d, ip, iq, v, lp, lq);
+        };
+        token = v0 + find_mass(kChunk, one, mark, before, s_sum, s_int, &s_before);
     }
     for (int i = tid; i <= a.width; i += kThreads)
         a.out_tokens[(size_t)seq * (a.width + 1) + i] = i < d.accepted ? a.tokens[seq * a.width + i] : i == d.accepted ? token : -1;
@@ -226,27 +489,37 @@ __global__ __launch_bounds__(kThreads) void verify_pick_kernel(VerifyArgs a, int
 }
 
 int slabs_of(int vocab) { return (vocab + kSlab - 1) / kSlab; }
-size_t parts_bytes(int seqs, int width, int vocab)
+
+// Parts of all rows, then the masses of chunks and slabs, in 8-byte words.
+struct Space {
+    size_t parts, chunks, slab_r, bytes;
+};
+Space space_of(int seqs, int width, int vocab)
 {
-    return (size_t)seqs * (2 * width + 1) * slabs_of(vocab) * sizeof(Part);
+    const size_t slabs = slabs_of(vocab);
+    Space s;
+    s.parts = 0;
+    s.chunks = (size_t)seqs * (2 * width + 1) * slabs * sizeof(Part);
+    s.slab_r = s.chunks + (width ? (size_t)seqs * slabs * kChunks * sizeof(double) : 0);
+    s.bytes = s.slab_r + (width ? (size_t)seqs * slabs * sizeof(double) : 0);
+    return s;
 }
 
 }  // namespace
 
-size_t verify_workspace(int seqs, int width, int vocab)
-{
-    return parts_bytes(seqs, width, vocab) + (size_t)seqs * slabs_of(vocab) * sizeof(double2);
-}
+size_t verify_workspace(int seqs, int width, int vocab) { return space_of(seqs, width, vocab).bytes; }
 
 hipError_t launch_verify(const VerifyArgs &a, void *workspace, hipStream_t st)
 {
     const int slabs = slabs_of(a.vocab);
-    Part *parts = static_cast<Part *>(workspace);
-    double2 *masses = reinterpret_cast<double2 *>(static_cast<char *>(workspace) + parts_bytes(a.seqs, a.width, a.vocab));
+    const Space sp = space_of(a.seqs, a.width, a.vocab);
+    char *ws = static_cast<char *>(workspace);
+    Part *parts = reinterpret_cast<Part *>(ws + sp.parts);
+    double *chunks = reinterpret_cast<double *>(ws + sp.chunks), *slab_r = reinterpret_cast<double *>(ws + sp.slab_r);
     const int rows = a.seqs * (a.draft ? 2 * a.width + 1 : a.width + 1);
     verify_stats_kernel<<<rows * slabs, kThreads, 0, st>>>(a, slabs, parts);
-    verify_mass_kernel<<<a.seqs * slabs, kThreads, 0, st>>>(a, slabs, parts, masses);
-    verify_pick_kernel<<<a.seqs, kThreads, 0, st>>>(a, slabs, parts, masses);
+    if (a.width) verify_mass_kernel<<<a.seqs * slabs, kThreads, 0, st>>>(a, slabs, parts, chunks, slab_r);
+    verify_pick_kernel<<<a.seqs, kThreads, 0, st>>>(a, slabs, parts, chunks, slab_r);
     return hipGetLastError();
 }
 
