@@ -254,17 +254,30 @@ __global__ __launch_bounds__(kThreads) void verify_stats_kernel(VerifyArgs a, in
     if (threadIdx.x == 0) parts[(size_t)row * slabs + slab] = Part{sum, top, at};
 }
 
-// A row's largest logit, its place and the sum of its exponentials, from its
-// slabs; by one wave.
-__device__ __forceinline__ Part row_of(const Part *p, int slabs)
+// A row's largest logit and the first place of it (greedy), or the sum of its
+// exponentials, from its slabs; by one wave.
+__device__ __forceinline__ Part row_of(const Part *p, int slabs, bool first_only)
 {
     const int lane = threadIdx.x & 63;
-    Part r{0.0, -INFINITY, 0x7FFFFFFF};
-    for (int i = lane; i < slabs; i += 64) larger(r.top, r.at, p[i].top, p[i].at);
+    const Part none{0.0, -INFINITY, 0x7FFFFFFF};
+    const Part mine = lane < slabs ? p[lane] : none;   // all of them, up to half a million tokens
+    Part r = none;
+    r.top = mine.top;
+    for (int i = lane + 64; i < slabs; i += 64) r.top = fmaxf(r.top, p[i].top);
 #pragma unroll
-    for (int off = 32; off; off >>= 1) larger(r.top, r.at, __shfl_xor(r.top, off, 64), __shfl_xor(r.at, off, 64));
-    if (r.top > -INFINITY)
-        for (int i = lane; i < slabs; i += 64) r.sum += p[i].sum * term(p[i].top, r.top);
+    for (int off = 32; off; off >>= 1) r.top = fmaxf(r.top, __shfl_xor(r.top, off, 64));
+    if (!(r.top > -INFINITY)) return r;
+    if (first_only) {
+        if (mine.top == r.top) r.at = mine.at;
+        for (int i = lane + 64; i < slabs; i += 64)
+            if (p[i].top == r.top) r.at = min(r.at, p[i].at);
+#pragma unroll
+        for (int off = 32; off; off >>= 1) r.at = min(r.at, __shfl_xor(r.at, off, 64));
+        return r;
+    }
+    r.sum = mine.sum > 0.0 ? mine.sum * term(mine.top, r.top) : 0.0;
+    for (int i = lane + 64; i < slabs; i += 64)
+        if (p[i].sum > 0.0) r.sum += p[i].sum * term(p[i].top, r.top);
     r.sum = wave_sum64(r.sum);
     return r;
 }
@@ -316,7 +329,7 @@ __device__ __forceinline__ Decision decide(const VerifyArgs &a, const Part *part
     const int rows = d.drafts + 1 + (have_q ? d.drafts : 0);
     for (int i = wave; i < rows; i += kWaves) {
         const bool t = i <= d.drafts;
-        const Part r = row_of(t ? pt + (size_t)i * slabs : pd + (size_t)(i - d.drafts - 1) * slabs, slabs);
+        const Part r = row_of(t ? pt + (size_t)i * slabs : pd + (size_t)(i - d.drafts - 1) * slabs, slabs, d.first_only);
         if (lane == 0) (t ? s.p[i] : s.q[i - d.drafts - 1]) = r;
     }
     __syncthreads();
@@ -364,12 +377,13 @@ __device__ __forceinline__ double token_r(const VerifyArgs &a, const Decision &d
 __device__ __forceinline__ double inverse(double s) { return s > 0.0 ? 1.0 / s : 0.0; }
 
 // The masses of r: chunks[seq][slab][kChunks] and slabs_r[seq][slab].
-__global__ __launch_bounds__(kThreads) void verify_mass_kernel(VerifyArgs a, int slabs, const Part *parts, double *chunks, double *slab_r)
+__global__ __launch_bounds__(kThreads) void verify_mass_kernel(VerifyArgs a, int slabs, const Part *parts, double *chunks, double *slab_r, Decision *decisions)
 {
     __shared__ DecisionSpace s;
     __shared__ double s_sum[kWaves];
     const int seq = blockIdx.x / slabs, slab = blockIdx.x - seq * slabs, v0 = slab * kSlab;
     const Decision d = decide(a, parts, slabs, seq, s);
+    if (slab == 0 && threadIdx.x == 0) decisions[seq] = d;
     if (d.first_only || !(d.q.sum > 0.0)) return;   // the largest, or p itself
     float lp[kTurns][4], lq[kTurns][4];
     load_slab(target_row(a, seq, d.accepted), v0, a.vocab, lp);
@@ -395,63 +409,79 @@ __global__ __launch_bounds__(kThreads) void verify_mass_kernel(VerifyArgs a, int
 }
 
 // The first of `count` masses up to which their sum, with `before`, exceeds
-// `mark`; else the last that is not zero (rounding).  before: becomes the sum of
-// those ahead of it.  By all threads.
+// `mark`; else the last that is not zero (rounding), -1 if all are.  before:
+// becomes the sum of those ahead of it.  By one wave, the same for every lane;
+// `mine`: the mass of this lane's place in the first 64.
 template <class Mass>
-__device__ __forceinline__ int find_mass(int count, Mass mass, double mark, double &before, double *s_sum, int *s_int, double *s_before)
+__device__ __forceinline__ int find_mass(int count, Mass mass, double mine, double mark, double &before)
 {
-    int found = 0x7FFFFFFF, last = -1;
-    for (int i0 = 0; i0 < count && found == 0x7FFFFFFF; i0 += kThreads) {
-        const int i = i0 + threadIdx.x;
-        const double m = i < count ? mass(i) : 0.0;
-        double total;
-        const double run = before + block_scan(m, s_sum, total);
-        found = block_min(m > 0.0 && run > mark ? i : 0x7FFFFFFF, s_int);
-        const int l = -block_min(m > 0.0 ? -i : 1, s_int);
-        if (l >= 0) last = l;
-        const int mine = found != 0x7FFFFFFF ? found : l;
-        if (mine == i) *s_before = run - m;
-        __syncthreads();
-        if (found == 0x7FFFFFFF) before += total;
+    const int lane = threadIdx.x & 63;
+    double ahead = before, last_ahead = before;
+    int last = -1;
+    for (int i0 = 0; i0 < count; i0 += 64) {
+        const int i = i0 + lane;
+        const double m = i0 == 0 ? mine : i < count ? mass(i) : 0.0;
+        double run = m;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const double o = __shfl_up(run, off, 64);
+            if (lane >= off) run += o;
+        }
+        const double here = __shfl(run, 63, 64);
+        run += ahead;
+        const uint64_t some = __ballot(m > 0.0), over = __ballot(m > 0.0 && run > mark);
+        if (some) {
+            const int l = over ? __ffsll((unsigned long long)over) - 1 : 63 - __clzll((long long)some);
+            last = i0 + l;
+            last_ahead = __shfl(run - m, l, 64);
+        }
+        if (over) break;
+        ahead += here;
     }
-    if (last >= 0) before = *s_before;
-    __syncthreads();
-    return found != 0x7FFFFFFF ? found : last;
+    before = last_ahead;
+    return last;
 }
 
-// One workgroup per sequence.
-__global__ __launch_bounds__(kThreads) void verify_pick_kernel(VerifyArgs a, int slabs, const Part *parts, const double *chunks, const double *slab_r)
+// One workgroup per sequence; its first wave chooses.
+__global__ __launch_bounds__(kThreads) void verify_pick_kernel(VerifyArgs a, int slabs, const Part *parts, const double *chunks, const double *slab_r, const Decision *decisions)
 {
     __shared__ DecisionSpace s;
-    __shared__ double s_sum[kWaves], s_chunk[kChunks], s_before;
-    __shared__ int s_int[kWaves];
-    const int seq = blockIdx.x, tid = threadIdx.x;
-    const Decision d = decide(a, parts, slabs, seq, s);
+    __shared__ double s_chunk[kChunks], s_token[kChunk], s_before, s_mark;
+    __shared__ int s_slab, s_place, s_rest;
+    const int seq = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const Decision d = a.width ? decisions[seq] : decide(a, parts, slabs, seq, s);
     int token = -1;
     if (d.first_only) {
         token = d.p.top > -INFINITY ? d.p.at : -1;
     } else if (d.p.sum > 0.0) {
-        const Part *pt = parts + ((size_t)seq * (a.width + 1) + d.accepted) * slabs;
-        const double *mr = slab_r + (size_t)seq * slabs;
-        bool rest = d.q.sum > 0.0;
-        auto mass = [&](int i) { return rest ? mr[i] : pt[i].sum > 0.0 ? pt[i].sum * term(pt[i].top, d.p.top) : 0.0; };
-        auto sum_of = [&]() {
-            double all = 0.0, total;
-            for (int i = tid; i < slabs; i += kThreads) all += mass(i);
-            block_scan(all, s_sum, total);
-            return total;
-        };
-        double total = sum_of();
-        if (rest && !(total > 0.0)) {   // the draft has all that the target has
-            rest = false;
-            total = sum_of();
-        }
-        const double mark = (double)a.picks[seq] * total;
-        // (of p the masses are exp(l - top) here, without the division by their sum)
-        const double ip = rest ? inverse(d.p.sum) : 1.0, iq = inverse(d.q.sum);
-        double before = 0.0;
-        const int slab = find_mass(slabs, mass, mark, before, s_sum, s_int, &s_before);
         const Row rp = target_row(a, seq, d.accepted);
+        if (wave == 0) {
+            const Part *pt = parts + ((size_t)seq * (a.width + 1) + d.accepted) * slabs;
+            const double *mr = slab_r + (size_t)seq * slabs;
+            bool rest = d.q.sum > 0.0;
+            auto mass = [&](int i) { return rest ? mr[i] : pt[i].sum > 0.0 ? pt[i].sum * term(pt[i].top, d.p.top) : 0.0; };
+            double mine, total;
+            auto add = [&]() {
+                mine = lane < slabs ? mass(lane) : 0.0;
+                double all = mine;
+                for (int i = lane + 64; i < slabs; i += 64) all += mass(i);
+                total = wave_sum64(all);
+            };
+            add();
+            if (rest && !(total > 0.0)) {   // the draft has all that the target has
+                rest = false;
+                add();
+            }
+            double before = 0.0;
+            const double mark = (double)a.picks[seq] * total;
+            const int slab = find_mass(slabs, mass, mine, mark, before);
+            if (lane == 0) s_slab = slab, s_before = before, s_mark = mark, s_rest = rest;
+        }
+        __syncthreads();
+        const bool rest = s_rest;
+        const int slab = s_slab;
+        const double mark = s_mark;
+        // (of p the masses are exp(l - top) here, without the division by their sum)
         if (!rest) {
             float lp[kTurns][4];
             load_slab(rp, slab * kSlab, a.vocab, lp);
@@ -461,38 +491,49 @@ __global__ __launch_bounds__(kThreads) void verify_pick_kernel(VerifyArgs a, int
 #pragma unroll
                 for (int j = 0; j < 4; ++j) m += term(lp[k][j], d.p.top);
                 m = wave_sum64(m);
-                if ((tid & 63) == 0) s_chunk[k * kWaves + (tid >> 6)] = m;
+                if (lane == 0) s_chunk[k * kWaves + wave] = m;
             }
-        } else if (tid < kChunks) {
-            s_chunk[tid] = chunks[((size_t)seq * slabs + slab) * kChunks + tid];
+            __syncthreads();
+        }
+        double before = s_before;
+        if (wave == 0) {
+            const double mine = lane >= kChunks ? 0.0 : rest ? chunks[((size_t)seq * slabs + slab) * kChunks + lane] : s_chunk[lane];
+            const int chunk = find_mass(kChunks, [](int) { return 0.0; }, mine, mark, before);
+            if (lane == 0) s_place = slab * kSlab + chunk * kChunk;
         }
         __syncthreads();
-        const int chunk = find_mass(kChunks, [&](int i) { return s_chunk[i]; }, mark, before, s_sum, s_int, &s_before);
-        const int v0 = slab * kSlab + chunk * kChunk;
-        auto one = [&](int i) {
-            const int v = v0 + i;
-            if (v >= a.vocab) return 0.0;
+        const int v0 = s_place, v = v0 + tid;
+        double m = 0.0;
+        if (v < a.vocab) {
             const float lp = load_typed(rp.p, rp.type, v);
-            if (!rest) return term(lp, d.p.top);
-            float lq = 0.f;
-            if (a.draft) {
-                const Row rq = draft_row(a, seq, d.accepted);
-                lq = load_typed(rq.p, rq.type, v);
+            if (rest) {
+                float lq = 0.f;
+                if (a.draft) {
+                    const Row rq = draft_row(a, seq, d.accepted);
+                    lq = load_typed(rq.p, rq.type, v);
+                }
+                m = token_r(a, d, inverse(d.p.sum), inverse(d.q.sum), v, lp, lq);
+            } else {
+                m = term(lp, d.p.top);
             }
-            return token_r(a, d, ip, iq, v, lp, lq);
-        };
-        token = v0 + find_mass(kChunk, one, mark, before, s_sum, s_int, &s_before);
+        }
+        s_token[tid] = m;
+        __syncthreads();
+        // (the other waves' `before` is of no use, nor is what they find)
+        token = v0 + find_mass(kChunk, [&](int i) { return s_token[i]; }, s_token[lane], mark, before);
     }
-    for (int i = tid; i <= a.width; i += kThreads)
+    if (wave) return;
+    for (int i = lane; i <= a.width; i += 64)
         a.out_tokens[(size_t)seq * (a.width + 1) + i] = i < d.accepted ? a.tokens[seq * a.width + i] : i == d.accepted ? token : -1;
-    if (tid == 0) a.accepted[seq] = d.accepted;
+    if (lane == 0) a.accepted[seq] = d.accepted;
 }
+static_assert(kThreads == kChunk && kChunks <= 64, "a thread for each token of 256, a lane for each 256 of a slab");
 
 int slabs_of(int vocab) { return (vocab + kSlab - 1) / kSlab; }
 
-// Parts of all rows, then the masses of chunks and slabs, in 8-byte words.
+// Parts of all rows, the masses of chunks and slabs, the decisions; in whole 8-byte words.
 struct Space {
-    size_t parts, chunks, slab_r, bytes;
+    size_t parts, chunks, slab_r, decisions, bytes;
 };
 Space space_of(int seqs, int width, int vocab)
 {
@@ -501,7 +542,8 @@ Space space_of(int seqs, int width, int vocab)
     s.parts = 0;
     s.chunks = (size_t)seqs * (2 * width + 1) * slabs * sizeof(Part);
     s.slab_r = s.chunks + (width ? (size_t)seqs * slabs * kChunks * sizeof(double) : 0);
-    s.bytes = s.slab_r + (width ? (size_t)seqs * slabs * sizeof(double) : 0);
+    s.decisions = s.slab_r + (width ? (size_t)seqs * slabs * sizeof(double) : 0);
+    s.bytes = s.decisions + (width ? (size_t)seqs * sizeof(Decision) : 0);
     return s;
 }
 
@@ -516,10 +558,11 @@ hipError_t launch_verify(const VerifyArgs &a, void *workspace, hipStream_t st)
     char *ws = static_cast<char *>(workspace);
     Part *parts = reinterpret_cast<Part *>(ws + sp.parts);
     double *chunks = reinterpret_cast<double *>(ws + sp.chunks), *slab_r = reinterpret_cast<double *>(ws + sp.slab_r);
+    Decision *decisions = reinterpret_cast<Decision *>(ws + sp.decisions);
     const int rows = a.seqs * (a.draft ? 2 * a.width + 1 : a.width + 1);
     verify_stats_kernel<<<rows * slabs, kThreads, 0, st>>>(a, slabs, parts);
-    if (a.width) verify_mass_kernel<<<a.seqs * slabs, kThreads, 0, st>>>(a, slabs, parts, chunks, slab_r);
-    verify_pick_kernel<<<a.seqs, kThreads, 0, st>>>(a, slabs, parts, chunks, slab_r);
+    if (a.width) verify_mass_kernel<<<a.seqs * slabs, kThreads, 0, st>>>(a, slabs, parts, chunks, slab_r, decisions);
+    verify_pick_kernel<<<a.seqs, kThreads, 0, st>>>(a, slabs, parts, chunks, slab_r, decisions);
     return hipGetLastError();
 }
 
