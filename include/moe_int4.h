@@ -409,10 +409,15 @@ int32_t moe_int4_logits_process(const void *logits, int32_t logits_type, int64_t
  *   out       [tokens][n] of out_type, rows out_stride >= n elements apart;
  *             what lies between the rows is left as it was
  *   epilogue  may be NULL (out is then the plain product)
- * x is taken as bf16 unchanged.  Products are formed as x * (code + 24) less
- * 24 * x, exactly, and summed in fp32 group by group: values of x beyond 2^110
- * may overflow on the way, and a token with an infinity or a NaN in x has NaN
- * in all its own outputs (before activation and residual), and in no others.
+ * Numerics: neither x nor a weight is rounded to fewer bits where it counts.
+ * With few rows (below 32 to an expert always) products are formed as x * (code + 24) less
+ * 24 * x, exactly, and summed in fp32 group by group; values of x beyond 2^110
+ * may overflow on the way.  With many rows x and code * scale are taken as fp16
+ * values times a power of two of their own row: exact but for inputs below
+ * 2^-28 and scales below 2^-24 of the largest of their row, which are off by at
+ * most 2^-38 (x) and 2^-35 (scales) of that largest.  Either way a token with an
+ * infinity or a NaN in x has NaN in all its own products, and in no others; an
+ * infinite or NaN scale makes its row's outputs NaN or infinite.
  * group is 64 or 128, k a multiple of it (at most 65536), n in [1, 2^24],
  * tokens in [0, 2^20] with tokens * n and (tokens + 1) * (k rounded up to a
  * multiple of 128) below 2^31; tokens = 0 is a no-op.  Strides, alignment, overlaps, workspace and streams as in

@@ -511,8 +511,9 @@ __global__ __launch_bounds__(WAVES * kWave) void int4_tile_kernel(Int4Args g, In
     if (chunk >= pl.tiles || nb >= gr.nblocks) return;
     int e = 0, first, rows;
     if (g.offsets) {
-        if (chunk >= list[0].x) return;
-        const int4 t = list[1 + chunk];
+        const int count = list[0].x;
+        const int4 t = list[1 + chunk];   // (of a slot that is not filled it is not used)
+        if (chunk >= count) return;
         e = t.x, first = t.y, rows = t.z;
     } else {
         first = (int)((long)g.places * chunk / pl.tiles);
@@ -539,39 +540,17 @@ __global__ __launch_bounds__(WAVES * kWave) void int4_tile_kernel(Int4Args g, In
 #pragma unroll
     for (int o = 0; o < 4; ++o) copy_w(o >> 1, o >> 1, o & 1);
 
-    // The scales of a weight row are taken times a power of two that brings the
-    // largest finite one below 2^11: then 24 s, and with it code * s, is within
-    // fp16's range, and scales down to 2^-25 of it are exact.
-    const uint16_t *ws = g.ws + ((size_t)e * g.N + min(n0 + 32 * wave + c, g.N - 1)) * ng;
-    uint32_t sc[3][kGroups];
-    auto fetch = [&](int st, int set) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i) sc[set][i] = ws[min(st * kGroups + i, ng - 1)];
-    };
-    uint32_t top = 0;
-#pragma unroll 8
-    for (int i = h; i < ng; i += 2) {
-        const uint32_t b = ws[i] & 0x7F80u;
-        top = max(top, b == 0x7F80u ? 0u : b);
-    }
     for (int i = tid; i < kRows; i += NT) {
-        int at = pl.rows, o = -1;   // zeros, nowhere
+        int at = pl.rows;   // zeros
         if (i < rows) {
-            at = o = first + i;
+            at = first + i;
             if (!pl.by_place && g.gather) {
                 const int slot = g.gather[first + i];
                 at = slot < 0 ? pl.rows : min(slot / g.gather_div, pl.rows);
             }
-            if (g.scatter) o = g.scatter[first + i];
-            if (o < 0 || o >= g.out_rows) o = -1;
         }
         s.row[i] = at;
-        s.exp[i] = exps[at];
-        s.out[i] = o;
-        s.weight[i] = g.row_weights && o >= 0 ? g.row_weights[o] : 1.f;
     }
-    top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-    const int wshift = 137 - max((int)(top >> 7), 1);
     __syncthreads();
 
     // x: copy o of a wave takes rows 4 (WAVES o + wave) .. + 3, lane l piece (l
@@ -586,6 +565,40 @@ __global__ __launch_bounds__(WAVES * kWave) void int4_tile_kernel(Int4Args g, In
     auto copy_x = [&](int st, int buf, int o) __attribute__((always_inline)) {
         load_to_lds<16>(x_buf, src[o], 2 * kStageK * min(st, stages - 1), s.x[buf] + 4 * (WAVES * o + wave) * kStageK);
     };
+#pragma unroll
+    for (int o = 0; o < kX; ++o) copy_x(0, 0, o);
+    if (kBufs == 3)
+#pragma unroll
+        for (int o = 0; o < kX; ++o) copy_x(1, 1, o);
+
+    // The scales of a weight row are taken times a power of two that brings the
+    // largest finite one below 2^11: then 24 s, and with it code * s, is within
+    // fp16's range, and scales down to 2^-24 of it are exact.
+    const uint16_t *ws = g.ws + ((size_t)e * g.N + min(n0 + 32 * wave + c, g.N - 1)) * ng;
+    uint32_t sc[3][kGroups];
+    auto fetch = [&](int st, int set) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) sc[set][i] = ws[min(st * kGroups + i, ng - 1)];
+    };
+    uint32_t top = 0;
+#pragma unroll 8
+    for (int i = h; i < ng; i += 2) {
+        const uint32_t b = ws[i] & 0x7F80u;
+        top = max(top, b == 0x7F80u ? 0u : b);
+    }
+    // what the epilogue needs of the rows, while their x is on its way
+    for (int i = tid; i < kRows; i += NT) {
+        int o = -1;   // nowhere
+        if (i < rows) {
+            o = g.scatter ? g.scatter[first + i] : first + i;
+            if (o < 0 || o >= g.out_rows) o = -1;
+        }
+        s.exp[i] = exps[s.row[i]];
+        s.out[i] = o;
+        s.weight[i] = g.row_weights && o >= 0 ? g.row_weights[o] : 1.f;
+    }
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+    const int wshift = 137 - max((int)(top >> 7), 1);
 
     f32x16_t acc[MAXMA];
 #pragma unroll
@@ -656,13 +669,8 @@ __global__ __launch_bounds__(WAVES * kWave) void int4_tile_kernel(Int4Args g, In
     auto all = [&](auto ma_c) __attribute__((always_inline)) {
         fetch(0, 0);
         fetch(1, 1);
-#pragma unroll
-        for (int o = 0; o < kX; ++o) copy_x(0, 0, o);
-        if (kBufs == 3)
-#pragma unroll
-            for (int o = 0; o < kX; ++o) copy_x(1, 1, o);
         fetch(2, 2);
-        wait_loads<(kBufs == 3 ? kX : 0) + kGroups>();   // the first stage's: fewer follow it than later ones'
+        wait_loads<3 * kGroups>();   // the first copies: fewer loads follow them than later ones
         if constexpr (kBufs == 3) {
             for (int st = 0; st < stages; st += 3) {
                 stage(ma_c, st, 0, 0);
@@ -693,12 +701,13 @@ __global__ __launch_bounds__(WAVES * kWave) void int4_tile_kernel(Int4Args g, In
     // 32 rows at a time through LDS, so that a thread has four columns of a row;
     // one body for all row tiles, for its code is fetched anew at every launch
     constexpr int kPitch = kCols + 4, kPer = 32 * kCols / 4 / NT;   // rows of a thread
-    static_assert(sizeof(float) * 32 * kPitch <= sizeof(s.x), "staging of the epilogue");
-    float *s_y = reinterpret_cast<float *>(s.x);
+    static_assert(2 * sizeof(float) * 32 * kPitch <= sizeof(s.x), "staging of the epilogue");
     const int col = 4 * (tid % (kCols / 4)), n = n0 + col, row0 = tid / (kCols / 4);
 #pragma unroll 1
     for (int m = 0; m < mtiles; ++m) {
-        __syncthreads();
+        if (m == 0) __syncthreads();   // every wave's last reads of x
+        // two places in turn: a wave writes the next rows while others read
+        float *s_y = reinterpret_cast<float *>(s.x) + (m & 1) * (32 * kPitch);
 #pragma unroll
         for (int mm = 0; mm < MAXMA; ++mm)
             if (m == mm)

@@ -76,34 +76,40 @@ __device__ __forceinline__ void larger(float &top, int &at, float other, int pla
     }
 }
 
+// Sum over the wave, the same for every lane, in a fixed order.
+template <int CTRL>
+__device__ __forceinline__ double dpp_move64(double v)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xF, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double read_lane64(double v, int l)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, l), hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), l);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 __device__ __forceinline__ double wave_sum64(double v)
 {
-#pragma unroll
-    for (int off = 32; off; off >>= 1) v += __shfl_xor(v, off, 64);
-    return v;
+    v += dpp_move64<kDppXor1>(v);
+    v += dpp_move64<kDppXor2>(v);
+    v += dpp_move64<kDppHalfMirror>(v);
+    v += dpp_move64<kDppMirror>(v);
+    return (read_lane64(v, 0) + read_lane64(v, 16)) + (read_lane64(v, 32) + read_lane64(v, 48));
 }
 
-// The sums of this thread and of those before it in the workgroup, in a fixed
-// order; total: of all.
-__device__ __forceinline__ double block_scan(double v, double *s, double &total)
+// The workgroup's, for its first thread.
+__device__ __forceinline__ double block_sum(double v, double *s)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const double o = __shfl_up(v, off, 64);
-        if (lane >= off) v += o;
-    }
+    v = wave_sum64(v);
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
     __syncthreads();
-    if (lane == 63) s[wave] = v;
-    __syncthreads();
-    double base = 0.0;
-    total = 0.0;
+    v = s[0];
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        if (w < wave) base += s[w];
-        total += s[w];
-    }
-    return base + v;
+    for (int w = 1; w < kWaves; ++w) v += s[w];
+    return v;
 }
 
 // The smallest of a workgroup's ints.
@@ -243,13 +249,13 @@ __global__ __launch_bounds__(kThreads) void verify_stats_kernel(VerifyArgs a, in
         for (int k = 0; k < kTurns; ++k)
 #pragma unroll
             for (int j = 0; j < 4; ++j) sum += l[k][j] == top ? 1.0 : 0.0;
-        block_scan(sum, s_sum, sum);
+        sum = block_sum(sum, s_sum);
     } else if (top > -INFINITY) {
 #pragma unroll
         for (int k = 0; k < kTurns; ++k)
 #pragma unroll
             for (int j = 0; j < 4; ++j) sum += exp_below((double)l[k][j] - (double)top);
-        block_scan(sum, s_sum, sum);
+        sum = block_sum(sum, s_sum);
     }
     if (threadIdx.x == 0) parts[(size_t)row * slabs + slab] = Part{sum, top, at};
 }
@@ -377,7 +383,7 @@ __device__ __forceinline__ double token_r(const VerifyArgs &a, const Decision &d
 __device__ __forceinline__ double inverse(double s) { return s > 0.0 ? 1.0 / s : 0.0; }
 
 // The masses of r: chunks[seq][slab][kChunks] and slabs_r[seq][slab].
-__global__ __launch_bounds__(kThreads) void verify_mass_kernel(VerifyArgs a, int slabs, const Part *parts, double *chunks, double *slab_r, Decision *decisions)
+__global__ __launch_bounds__(kThreads, 4) void verify_mass_kernel(VerifyArgs a, int slabs, const Part *parts, double *chunks, double *slab_r, Decision *decisions)
 {
     __shared__ DecisionSpace s;
     __shared__ double s_sum[kWaves];
@@ -403,6 +409,7 @@ __global__ __launch_bounds__(kThreads) void verify_mass_kernel(VerifyArgs a, int
     if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = all;
     __syncthreads();
     if (threadIdx.x == 0) {
+#pragma unroll
         for (int w = 1; w < kWaves; ++w) all += s_sum[w];
         slab_r[(size_t)seq * slabs + slab] = all;
     }
