@@ -216,7 +216,8 @@ __global__ __launch_bounds__(KS * WC * kWave) void int4_rows_kernel(Int4Args g, 
     const rsrc_t w_buf = buffer_of(g.wq + ((size_t)e * g.N + min(nw, g.N - 1)) * kw, (uint32_t)nrows * (uint32_t)kw * 4u);
     const uint32_t wsrc = 4u * (uint32_t)(lane >> 2) * (uint32_t)kw + 16 * ((lane & 3) ^ (lane >> 4 & 3));
     // (without gather the rows are consecutive: their first is the buffer's)
-    const rsrc_t x_buf = buffer_of(g.x + (g.gather ? 0 : (size_t)first * g.x_stride), 0xFFFFFFFFu);
+    const rsrc_t x_buf = buffer_of(g.x + (g.gather ? 0 : (size_t)first * g.x_stride),
+                                   2u * ((uint32_t)((g.gather ? g.x_rows : rows) - 1) * (uint32_t)g.x_stride + (uint32_t)g.K));
     uint32_t xsrc[kXCopies];
     int slot[kXCopies];
     auto copied = [&](int i) __attribute__((always_inline)) { return WC == 1 ? i : (wc + i * WC) % (XR / 4); };   // which of x
@@ -228,15 +229,14 @@ __global__ __launch_bounds__(KS * WC * kWave) void int4_rows_kernel(Int4Args g, 
 #pragma unroll
     for (int i = 0; i < kXCopies; ++i) {   // (a row of zeros reads row 0 and is cleared at the end)
         const int xr = slot[i] < 0 ? 0 : slot[i] / g.gather_div;
-        xsrc[i] = 2u * (uint32_t)(xr < g.x_rows ? xr : 0) * (uint32_t)g.x_stride;
+        xsrc[i] = 2u * (uint32_t)(xr < g.x_rows ? xr : 0) * (uint32_t)g.x_stride + 16 * ((lane & 15) ^ (lane >> 4) ^ (4 * copied(i)));
     }
-    const int piece = (lane & 15) ^ (lane >> 4);
     auto copy = [&](int u, int buf) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) load_to_lds<16>(w_buf, wsrc + (uint32_t)(64 * t) * (uint32_t)kw, 64 * u, s.w[wave][buf] + t * 256);
 #pragma unroll
-        for (int i = 0; i < kXCopies; ++i)   // (half a unit at K's end: any inputs do, none are used)
-            load_to_lds<16>(x_buf, xsrc[i] + 2 * min(128 * u + 8 * (piece ^ (4 * copied(i))), g.K - 8), 0, s.x[ks][buf] + copied(i) * 512);
+        for (int i = 0; i < kXCopies; ++i)   // (half a unit at K's end: what comes behind it is not used)
+            load_to_lds<16>(x_buf, xsrc[i], 256 * u, s.x[ks][buf] + copied(i) * 512);
     };
     // scales of kAhead units, a lane a row
     auto scales = [&](int u) __attribute__((always_inline)) {
@@ -262,6 +262,11 @@ __global__ __launch_bounds__(KS * WC * kWave) void int4_rows_kernel(Int4Args g, 
     f32x4_t sum[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) sum[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    // The quarter of a group that lane quarter q takes.  LDS serves lanes 0-3,
+    // 12-15 and 20-27 of a half wave together, then the others: with quarters 0
+    // and 3 beside each other (and 1 and 2) those meet no bank twice, in order
+    // they met every one.  (Half groups, of 64, do in order.)
+    const int qk = G == 128 ? (q == 0 ? 0 : q == 1 ? 3 : q - 1) : q;
     auto compute = [&](int u, int buf) __attribute__((always_inline)) {
 #pragma unroll
         for (int a = 0; a < kGroups; ++a) {
@@ -270,14 +275,14 @@ __global__ __launch_bounds__(KS * WC * kWave) void int4_rows_kernel(Int4Args g, 
             f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < kWords; ++j) {
-                const int octet = (G / 8) * a + kWords * q + j, row = c % XR;
+                const int octet = (G / 8) * a + kWords * qk + j, row = c % XR;
                 xb[j] = pair_octet(*reinterpret_cast<const u32x4_t *>(s.x[ks][buf] + row * 128 + 8 * (octet ^ row)));
                 zero = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[j], minus24(), zero, 0, 0, 0);
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                // the lane's words: bytes 4 kWords q of the group's
-                const int byte = (G / 2) * a + 4 * kWords * q;
+                // the lane's words: bytes 4 kWords qk of the group's
+                const int byte = (G / 2) * a + 4 * kWords * qk;
                 const words_t w = *reinterpret_cast<const words_t *>(
                     s.w[wave][buf] + t * 256 + c * 16 + 4 * ((byte >> 4) ^ (c >> 2 & 3)) + (byte >> 2 & 3));
                 f32x4_t v = zero;
@@ -294,8 +299,7 @@ __global__ __launch_bounds__(KS * WC * kWave) void int4_rows_kernel(Int4Args g, 
     if (u0 + 1 < u1) copy(u0 + 1, 1);
     if constexpr (WC == 1) {
         // each wave by itself: a unit's place is free when its reads have ended
-        for (int u = u0; u < u1; ++u) {
-            const int buf = (u - u0) & 1;
+        auto unit = [&](int u, int buf) __attribute__((always_inline)) {
             if ((u - u0) % kAhead == 0) scales(u);
             __atomic_signal_fence(__ATOMIC_SEQ_CST);
             if (u + 1 < u1) wait_loads<kLoads>();
@@ -307,20 +311,28 @@ __global__ __launch_bounds__(KS * WC * kWave) void int4_rows_kernel(Int4Args g, 
                 wait_lds();
                 copy(u + 2, buf);
             }
+        };
+        for (int u = u0; u < u1; u += 2) {
+            unit(u, 0);
+            if (u + 1 < u1) unit(u + 1, 1);
         }
     } else {
         // x is shared: behind the barrier a unit is there for every wave, and the
         // place of the one before it is free
-        for (int u = u0, buf = 0; u < u1; ++u) {
+        auto unit = [&](int u, int buf) __attribute__((always_inline)) {
             if ((u - u0) % kAhead == 0) scales(u);
             __atomic_signal_fence(__ATOMIC_SEQ_CST);
             if (u + 1 < u1) wait_loads<kLoads>();
             else wait_loads<0>();
             __builtin_amdgcn_s_barrier();
             __atomic_signal_fence(__ATOMIC_SEQ_CST);
-            if (u + 2 < u1) copy(u + 2, buf == 0 ? 2 : buf - 1);
+            if (u + 2 < u1) copy(u + 2, (buf + 2) % 3);
             compute(u, buf);
-            buf = buf == 2 ? 0 : buf + 1;
+        };
+        for (int u = u0; u < u1; u += 3) {
+            unit(u, 0);
+            if (u + 1 < u1) unit(u + 1, 1);
+            if (u + 2 < u1) unit(u + 2, 2);
         }
     }
     __syncthreads();
