@@ -415,7 +415,8 @@ int32_t moe_int4_logits_process(const void *logits, int32_t logits_type, int64_t
  * may overflow on the way.  With many rows x and code * scale are taken as fp16
  * values times a power of two of their own row: exact but for inputs below
  * 2^-28 and scales below 2^-24 of the largest of their row, which are off by at
- * most 2^-38 (x) and 2^-35 (scales) of that largest.  Either way a token with an
+ * most 2^-38 (x) and 2^-35 (scales) of that largest.  Subnormal values of x and
+ * of the scales may count as zero.  Either way a token with an
  * infinity or a NaN in x has NaN in all its own products, and in no others; an
  * infinite or NaN scale makes its row's outputs NaN or infinite.
  * group is 64 or 128, k a multiple of it (at most 65536), n in [1, 2^24],

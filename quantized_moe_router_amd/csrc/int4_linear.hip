@@ -152,6 +152,14 @@ struct Int4Tiles {
 // what the group's products leave there is sum x code, exact up to fp32's
 // additions.  The group's scale multiplies that sum in fp32, so neither x nor
 // a weight is ever rounded.
+//
+// What bounds it: memory where it is large (one token of [248320, 2560] 70 us,
+// 4.7 TB/s, the rate of a copy; 5120 places of 512 experts, [1280, 2560], 215 us,
+// 4.1 TB/s, with the vector ALU busy 55 % of the time), and the way through
+// its dependent loads where it is small (one token of [2560, 2560]: 5 us, of
+// which the matrix takes 0.7).  Straight to LDS against loads into registers in
+// the operands' order: 70 us against 82, and 12.6 against 15.0 for 32 tokens of
+// [10240, 2560].
 template <int G, int NT, int KS, int WC, int XR>
 __global__ __launch_bounds__(KS * WC * kWave) void int4_rows_kernel(Int4Args g, Int4Tiles tl, int nblocks)
 {
@@ -356,16 +364,32 @@ __global__ __launch_bounds__(KS * WC * kWave) void int4_rows_kernel(Int4Args g, 
 }
 
 // ---------------------------------------------------------------------------
-// Many rows.  A pass over x puts it in pair order and forms the groups' sums
-// times -24; then a workgroup takes a chunk of up to 32 MAXMA sorted rows of one
-// expert and 32 WAVES weight rows, 32 of them to a wave, as
-// v_mfma_f32_32x32x16_bf16 tiles.  K goes in stages of 128: the chunk's x
-// through double-buffered LDS (16-byte pieces, exclusive-or'ed by the row, so
-// that reads meet no bank twice), the codes straight into registers.
+// Many rows.  A pass over x writes it as fp16 in pair order, each row times a
+// power of two of its own; then a workgroup takes a chunk of up to 32 MAXMA
+// sorted rows of one expert and 32 WAVES weight rows, 32 of them to a wave, as
+// v_mfma_f32_32x32x16_f16 tiles whose sums stay in registers over all of K.  K
+// goes in stages of 128: x and codes straight into LDS (16-byte pieces,
+// exclusive-or'ed by the row, so that reads meet no bank twice), two stages
+// ahead.  A wave makes its 32 rows' weights once a stage, in registers, for all
+// row tiles.
+//
+// The scale goes into the fp16 weight, not onto a group's sum as in the kernel
+// above: there sixteen products with it per tile and group, and a sum of x per
+// row, cost more here than the three instructions a word more do (81920 places
+// of 512 experts, [1280, 2560]: 820 us against 749).
+//
+// What bounds it: at 81920 places (718 us, 747 TFLOP/s, 60 % of a large library
+// product) the matrix cores are busy 42 % of the cycles, the vector ALU 27 %, LDS
+// 25 %; waves wait two fifths of their time, most of it where a stage begins:
+// a barrier, the first reads of LDS and the first weights follow each other
+// (about 1300 cycles of a stage's 3400 with 128 rows; a row tile more costs what
+// its products cost).  512 tokens of [10240, 2560] (49 us): 160 workgroups for 256
+// CUs besides, and 11 us of the pass over x, the start and the end.
 // ---------------------------------------------------------------------------
 constexpr int kStageK = 128;
 
-// What the pass over x leaves in the workspace.
+// What the pass over x leaves in the workspace.  It takes 5 us for 512 rows of
+// 2560, 22 us for 8192.
 struct Int4Plan {
     int rows;       // rows of xp: those of x, or the places where x has more; and one of zeros behind them
     bool by_place;
@@ -375,9 +399,6 @@ struct Int4Plan {
     size_t exps_at, list_at, bytes;
 };
 
-// Words of a lane for one stage: lane half h takes the 16-byte pieces h and 2 +
-// h of a row's 64 bytes; word w of piece p holds inputs 64 p + 32 h + 8 w ..
-// + 7, which is octet 8 p + 4 h + w of the stage.
 // The tiles of each expert, in its order: nearly equal parts of at most `most`
 // rows.  One workgroup of 256; list[0].x: how many.
 __device__ inline void list_tiles(const Int4Args &g, int most, int slots, int4 *list)
@@ -636,6 +657,8 @@ __global__ __launch_bounds__(WAVES * kWave) void int4_tile_kernel(Int4Args g, In
         // made from it are formed anew instead of held over all stages
         uint32_t at = 2 * kStageK * c + 16 * ((c & 15) ^ (4 * h));
         asm volatile("" : "+v"(at));
+        // lane half h takes pieces h and 2 + h of its weight row's 64 bytes; word
+        // j of the p-th holds the inputs of octet 8 p + 4 h + j of the stage
         u32x4_t wv[2];
 #pragma unroll
         for (int p = 0; p < 2; ++p)
