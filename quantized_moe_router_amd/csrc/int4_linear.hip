@@ -85,46 +85,103 @@ __device__ __forceinline__ void finish_int4(const Int4Args &g, int expert, int o
     store_typed(e.out, e.out_type, o * e.out_stride + r, v);
 }
 
-// Columns r .. r + 3 of P rows o (below 0: none) with their weights f.  The
-// residual of all rows is asked for first, so that it is waited for once.
+// Columns r, r + step, .. (four, those below N) of P rows o (below 0: none).
+template <int TYPE, int P>
+__device__ __forceinline__ void store_columns(const Int4Args &g, const int (&o)[P], int r, int step, const float4 (&v)[P])
+{
+    constexpr int kBytes = TYPE == kF32 ? 4 : 2;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        if (o[i] < 0) continue;
+        char *row = static_cast<char *>(g.e.out) + (o[i] * g.e.out_stride + r) * kBytes;
+        const float y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (r + j * step < g.N) store_typed(row + j * step * kBytes, TYPE, 0, y[j]);
+    }
+}
+
+// The same columns of the residual.
+template <int TYPE, int P>
+__device__ __forceinline__ void load_columns(const Int4Args &g, const int (&o)[P], int r, int step, float4 (&v)[P])
+{
+    constexpr int kBytes = TYPE == kF32 ? 4 : 2;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const char *row = static_cast<const char *>(g.e.residual) + max(o[i], 0) * g.e.residual_stride * kBytes;
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = load_typed(row, TYPE, min(r + j * step, g.N - 1));
+        v[i] = make_float4(y[0], y[1], y[2], y[3]);
+    }
+}
+
+// Columns r .. r + 3 of P rows, as one word.
+template <int TYPE, int P>
+__device__ __forceinline__ void store_words(const Int4Args &g, const int (&o)[P], int r, const float4 (&v)[P])
+{
+    constexpr int kBytes = TYPE == kF32 ? 4 : 2;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        if (o[i] >= 0) store_typed4(static_cast<char *>(g.e.out) + (o[i] * g.e.out_stride + r) * kBytes, TYPE, 0, v[i]);
+}
+
+// Four columns of P rows o (below 0: none) with their weights f: r .. r + 3 where
+// such words are aligned, else r, r + step, .., so that the lanes of a row move
+// consecutive elements.  The residual of all rows is asked for first, so that it
+// is waited for once.
 template <int P>
-__device__ __forceinline__ void finish_rows_int4(const Int4Args &g, int expert, const int (&o)[P], const float (&f)[P], int r, float4 (&v)[P])
+__device__ __forceinline__ void finish_rows_int4(const Int4Args &g, int expert, const int (&o)[P], const float (&f)[P], int r, int step, float4 (&v)[P])
 {
     const Int8Epilogue &e = g.e;
     if (!e.vec) {
+        if (e.bias || e.residual || e.activation != kActNone || g.row_weights) {
+            float4 res[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) res[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (e.residual) {
+                if (e.residual_type == kF32) load_columns<kF32>(g, o, r, step, res);
+                else if (e.residual_type == kBf16) load_columns<kBf16>(g, o, r, step, res);
+                else load_columns<kF16>(g, o, r, step, res);
+            }
 #pragma unroll 1
-        for (int j = 0; j < 4 && r + j < g.N; ++j) {
-            const float b = e.bias ? load_typed(e.bias, e.bias_type, (size_t)expert * g.N + r + j) : 0.f;
-            float res[P];
+            for (int j = 0; j < 4; ++j) {
+                const float b = e.bias ? load_typed(e.bias, e.bias_type, (size_t)expert * g.N + min(r + j * step, g.N - 1)) : 0.f;
 #pragma unroll
-            for (int i = 0; i < P; ++i)
-                res[i] = e.residual && o[i] >= 0 ? load_typed(e.residual, e.residual_type, o[i] * e.residual_stride + r + j) : 0.f;
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                float y = activate(v[i].x + b, e.activation) * f[i];
-                if (e.residual) y += res[i];
-                if (o[i] >= 0) store_typed(e.out, e.out_type, o[i] * e.out_stride + r + j, y);
-                v[i] = make_float4(v[i].y, v[i].z, v[i].w, 0.f);
+                for (int i = 0; i < P; ++i) {
+                    float y = activate(v[i].x + b, e.activation) * f[i];
+                    if (e.residual) y += res[i].x;
+                    v[i] = make_float4(v[i].y, v[i].z, v[i].w, y);   // four turns: in order again
+                    res[i] = make_float4(res[i].y, res[i].z, res[i].w, 0.f);
+                }
             }
         }
+        if (e.out_type == kF32) store_columns<kF32>(g, o, r, step, v);
+        else if (e.out_type == kBf16) store_columns<kBf16>(g, o, r, step, v);
+        else store_columns<kF16>(g, o, r, step, v);
         return;
     }
-    float4 res[P];
-    if (e.residual)
+    if (e.bias || e.residual || e.activation != kActNone || g.row_weights) {
+        float4 res[P];
+        if (e.residual)
 #pragma unroll
-        for (int i = 0; i < P; ++i) res[i] = load_typed4(e.residual, e.residual_type, max(o[i], 0) * e.residual_stride + min(r, g.N - 4));
-    float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (e.bias) b = load_typed4(e.bias, e.bias_type, (size_t)expert * g.N + min(r, g.N - 4));
+            for (int i = 0; i < P; ++i) res[i] = load_typed4(e.residual, e.residual_type, max(o[i], 0) * e.residual_stride + min(r, g.N - 4));
+        float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (e.bias) b = load_typed4(e.bias, e.bias_type, (size_t)expert * g.N + min(r, g.N - 4));
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        float4 y = make_float4(v[i].x + b.x, v[i].y + b.y, v[i].z + b.z, v[i].w + b.w);
-        if (e.activation != kActNone)
-            y = make_float4(activate(y.x, e.activation), activate(y.y, e.activation), activate(y.z, e.activation),
-                            activate(y.w, e.activation));
-        y = make_float4(y.x * f[i], y.y * f[i], y.z * f[i], y.w * f[i]);
-        if (e.residual) y = make_float4(y.x + res[i].x, y.y + res[i].y, y.z + res[i].z, y.w + res[i].w);
-        if (o[i] >= 0) store_typed4(e.out, e.out_type, o[i] * e.out_stride + r, y);
+        for (int i = 0; i < P; ++i) {
+            float4 y = make_float4(v[i].x + b.x, v[i].y + b.y, v[i].z + b.z, v[i].w + b.w);
+            if (e.activation != kActNone)
+                y = make_float4(activate(y.x, e.activation), activate(y.y, e.activation), activate(y.z, e.activation),
+                                activate(y.w, e.activation));
+            y = make_float4(y.x * f[i], y.y * f[i], y.z * f[i], y.w * f[i]);
+            if (e.residual) y = make_float4(y.x + res[i].x, y.y + res[i].y, y.z + res[i].z, y.w + res[i].w);
+            v[i] = y;
+        }
     }
+    if (e.out_type == kF32) store_words<kF32>(g, o, r, v);
+    else if (e.out_type == kBf16) store_words<kBf16>(g, o, r, v);
+    else store_words<kF16>(g, o, r, v);
 }
 
 // Which rows a workgroup takes: `count` tiles of at most 16 rows of one expert.
@@ -737,7 +794,7 @@ __global__ __launch_bounds__(WAVES * kWave) void int4_tile_kernel(Int4Args g, In
     // one body for all row tiles, for its code is fetched anew at every launch
     constexpr int kPitch = kCols + 4, kPer = 32 * kCols / 4 / NT;   // rows of a thread
     static_assert(2 * sizeof(float) * 32 * kPitch <= sizeof(s.x), "staging of the epilogue");
-    const int col = 4 * (tid % (kCols / 4)), n = n0 + col, row0 = tid / (kCols / 4);
+    const int col = (g.e.vec ? 4 : 1) * (tid % (kCols / 4)), n = n0 + col, row0 = tid / (kCols / 4);
 #pragma unroll 1
     for (int m = 0; m < mtiles; ++m) {
         if (m == 0) __syncthreads();   // every wave's last reads of x
@@ -760,9 +817,11 @@ __global__ __launch_bounds__(WAVES * kWave) void int4_tile_kernel(Int4Args g, In
             const int row = row0 + i * (NT / (kCols / 4));
             o[i] = n < g.N ? s.out[32 * m + row] : -1;
             f[i] = s.weight[32 * m + row];
-            v[i] = *reinterpret_cast<const float4 *>(s_y + row * kPitch + col);
+            const float *y = s_y + row * kPitch + col;
+            if (g.e.vec) v[i] = *reinterpret_cast<const float4 *>(y);
+            else v[i] = make_float4(y[0], y[kCols / 4], y[2 * (kCols / 4)], y[3 * (kCols / 4)]);
         }
-        finish_rows_int4(g, e, o, f, n, v);
+        finish_rows_int4(g, e, o, f, n, kCols / 4, v);
     }
 }
 
