@@ -213,10 +213,10 @@ struct Int4Tiles {
 // What bounds it: memory where it is large (one token of [248320, 2560] 70 us,
 // 4.7 TB/s, the rate of a copy; 5120 places of 512 experts, [1280, 2560], 215 us,
 // 4.1 TB/s, with the vector ALU busy 55 % of the time), and the way through
-// its dependent loads where it is small (one token of [2560, 2560]: 5 us, of
+// its dependent loads where it is small (one token of [2560, 2560]: 6 us, of
 // which the matrix takes 0.7).  Straight to LDS against loads into registers in
 // the operands' order: 70 us against 82, and 12.6 against 15.0 for 32 tokens of
-// [10240, 2560].
+// [10240, 2560] (10.9 with two column tiles a wave).
 template <int G, int NT, int KS, int WC, int XR>
 __global__ __launch_bounds__(KS * WC * kWave) void int4_rows_kernel(Int4Args g, Int4Tiles tl, int nblocks)
 {
@@ -435,7 +435,7 @@ __global__ __launch_bounds__(KS * WC * kWave) void int4_rows_kernel(Int4Args g, 
 // row, cost more here than the three instructions a word more do (81920 places
 // of 512 experts, [1280, 2560]: 820 us against 749).
 //
-// What bounds it: at 81920 places (718 us, 747 TFLOP/s, 60 % of a large library
+// What bounds it: at 81920 places (690 us, 778 TFLOP/s, 62 % of a large library
 // product) the matrix cores are busy 42 % of the cycles, the vector ALU 27 %, LDS
 // 25 %; waves wait two fifths of their time, most of it where a stage begins:
 // a barrier, the first reads of LDS and the first weights follow each other
@@ -918,15 +918,18 @@ hipError_t launch_int4_linear(const Int4Args &a, void *workspace, hipStream_t st
         tl.count = a.offsets ? a.places : (a.places + 15) / 16;
     }
     // Enough columns to go round: the waves of a workgroup take columns and share
-    // x (640 places of 512 experts, [2560, 640]: 72 us, with K over the waves
-    // 118).  Fewer: they share K (8 tokens of [10240, 2560] 8.3 us against 15.9),
-    // and few: eight of them, with sixteen columns (1 token of [2560, 2560] 6.0
-    // us, with four and 64 columns 7.0).
+    // x (640 places of 512 experts, [2560, 640]: 70 us, with K over the waves
+    // 118).  Fewer: four of them share K (8 tokens of [10240, 2560] 7.8 us, with
+    // columns over the waves 15.9, with four column tiles a wave 8.2; 64 tokens
+    // 16.8, 21.6 and 18.7).  A long K of few columns takes eight, where columns
+    // are very few with one column tile a wave (16 tokens of [5120, 5120] 8.1 us
+    // against 9.5 with four; 32 of [33, 10240] 8.3, 14.3).
     const bool four = !a.offsets && a.places <= 4;
-    const long blocks = (long)tl.count * ((a.N + 63) / 64);
-    if (blocks >= 1024) four ? launch_rows<2, 1, 4, 4>(a, tl, st) : launch_rows<2, 1, 4, 16>(a, tl, st);
-    else if (blocks >= 128) four ? launch_rows<4, 4, 1, 4>(a, tl, st) : launch_rows<4, 4, 1, 16>(a, tl, st);
-    else four ? launch_rows<1, 8, 1, 4>(a, tl, st) : launch_rows<1, 8, 1, 16>(a, tl, st);
+    const long columns = (long)tl.count * ((a.N + 31) / 32);
+    if (columns >= 2048) four ? launch_rows<2, 1, 4, 4>(a, tl, st) : launch_rows<2, 1, 4, 16>(a, tl, st);
+    else if (a.K >= 4096 && columns <= 64) four ? launch_rows<1, 8, 1, 4>(a, tl, st) : launch_rows<1, 8, 1, 16>(a, tl, st);
+    else if (a.K >= 4096 && columns <= 256) four ? launch_rows<2, 8, 1, 4>(a, tl, st) : launch_rows<2, 8, 1, 16>(a, tl, st);
+    else four ? launch_rows<2, 4, 1, 4>(a, tl, st) : launch_rows<2, 4, 1, 16>(a, tl, st);
     return hipGetLastError();
 }
 
