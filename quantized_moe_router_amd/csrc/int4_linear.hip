@@ -740,6 +740,12 @@ __global__ __launch_bounds__(WAVES * kWave) void int4_tile_kernel(Int4Args g, In
         // the loads of the stage, spread over its steps: all at once, behind the
         // barrier, they would hold every wave up before its first product
         auto load = [&](int i) __attribute__((always_inline)) {
+            // kFlight counts on the order of the three kinds, and to the compiler
+            // a scale's load into a register is independent of copies into LDS
+            if (i == kX || i == kX + 2) {
+                __atomic_signal_fence(__ATOMIC_SEQ_CST);
+                __builtin_amdgcn_sched_barrier(0);
+            }
             if (i < kX) copy_x(kBufs == 3 ? st + 2 : st + 1, kBufs == 3 ? (set + 2) % 3 : xset ^ 1, i);
             else if (i < kX + 2) copy_w(st + 2, (set + 2) % 3, i - kX);
             else fetch(st + 3, set);
