@@ -1,0 +1,95 @@
+"""The kernel of many rows behind moe_int4_linear and moe_int4_grouped_linear
+over many stages of 128 inputs (its buffers of x and codes go round every two or
+three) and over chunks of one to six tiles of 32 rows.  Formula and tolerance as in test_gpu_int4_linear."""
+import pytest
+import torch
+
+from quantized_moe_router_amd import _binding as B
+from quantized_moe_router_amd.layer import Int4GroupedLinear, Int4Linear
+from test_gpu_int4_linear import check, formula, generator, say, tables, weights
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    B.lib()
+    yield
+
+
+def copies_x(need, rows, k):
+    """Whether a call with this workspace takes the kernel of many rows, which holds x there as
+    whole stages of fp16 values with a row of zeros behind them; lists of tiles are far smaller."""
+    return need >= 2 * (rows + 1) * ((k + 127) // 128 * 128)
+
+
+# more than 96 rows to an expert on average: chunks of up to 192
+OF_192 = [1, 33, 64, 65, 97, 128, 129, 191, 192, 193, 385]
+# 32 to 96: chunks of up to 128
+OF_128 = [1, 32, 33, 64, 65, 96, 97, 128, 129, 2, 31, 0, 40]
+
+
+@pytest.mark.parametrize("counts,N", [(OF_192, 1700), (OF_128, 3331)])
+@pytest.mark.parametrize("K,G", [(896, 64), (896, 128), (1600, 64), (1664, 128), (2560, 64), (2560, 128)])
+def test_many_stages(counts, N, K, G):
+    E = len(counts)
+    g = generator(K + G + E)
+    off, slots, P = tables(counts, seed=K)
+    say(f"many stages E={E} places={P} N={N} K={K} G={G}")
+    packed, scales = weights((E, N), K, G, g)
+    x = torch.randn(P, K, device="cuda", generator=g).to(torch.bfloat16)
+    bias = torch.randn(E, N, device="cuda", generator=g)
+    rw = torch.randn(P, device="cuda", generator=g)
+    layer = Int4GroupedLinear(packed, scales, G, bias=bias)
+    groups = B.make_groups(P, P, P, off, scatter=slots, row_weights=rw)
+    assert copies_x(B.moe_int4_grouped_linear_workspace_bytes(groups, N, K, G), P, K)
+    out = torch.full((P, N), 77.0, device="cuda")
+    layer.forward(x, off, scatter=slots, row_weights=rw, out=out)
+    ends = off.tolist()
+    for e in range(E):
+        a, b = ends[e], ends[e + 1]
+        if a == b:
+            continue
+        mine = slots[a:b].long()
+        want, tol = formula(x[a:b], packed[e], scales[e], G, "none", bias[e], rw[mine])
+        check(out[mine], want, tol, torch.float32, f"expert {e} of {b - a}")
+    for _ in range(3):
+        again = torch.full((P, N), 77.0, device="cuda")
+        layer.forward(x, off, scatter=slots, row_weights=rw, out=again)
+        assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("T,N,K,G", [(130, 11000, 2560, 128), (400, 5300, 1600, 64), (512, 5200, 10240, 128)])
+def test_many_stages_of_one_matrix(T, N, K, G):
+    g = generator(T)
+    packed, scales = weights((N,), K, G, g)
+    x = torch.randn(T, K, device="cuda", generator=g).to(torch.bfloat16)
+    assert copies_x(B.moe_int4_linear_workspace_bytes(T, N, K, G), T, K)
+    want, tol = formula(x, packed, scales, G, "none")
+    layer = Int4Linear(packed, scales, G)
+    out = layer.forward(x, out_dtype=torch.float32)
+    check(out, want, tol, torch.float32, f"T={T} N={N} K={K} G={G}")
+    for _ in range(3):
+        assert torch.equal(layer.forward(x, out_dtype=torch.float32), out)
+
+
+def test_many_rows_past_4_gib():
+    """Many rows of the last of 40 experts, whose codes lie more than 4 GiB behind the first's."""
+    E, N, K, G, rows = 40, 16384, 16384, 128, 1300
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GiB of GPU memory")
+    g = generator(44)
+    packed = torch.empty(E, N, K // 8, dtype=torch.int32, device="cuda")
+    for e in range(E):
+        packed[e] = torch.randint(-2**31, 2**31 - 1, (N, K // 8), dtype=torch.int32, device="cuda", generator=g)
+    scales = (torch.randn(E, N, K // G, device="cuda", generator=g) * 0.002).to(torch.bfloat16)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[E] = rows
+    groups = B.make_groups(rows, rows, rows, off)
+    assert copies_x(B.moe_int4_grouped_linear_workspace_bytes(groups, N, K, G), rows, K)
+    x = torch.randn(rows, K, device="cuda", generator=g).to(torch.bfloat16)
+    out = Int4GroupedLinear(packed, scales, G).forward(x, off, out_dtype=torch.float32)
+    pick = torch.arange(0, N, 97, device="cuda")
+    want, tol = formula(x, packed[E - 1][pick], scales[E - 1][pick], G, "none")
+    check(out[:, pick], want, tol, torch.float32, f"{rows} rows")
