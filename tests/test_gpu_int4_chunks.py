@@ -1,6 +1,7 @@
 """The kernel of many rows behind moe_int4_linear and moe_int4_grouped_linear
 over many stages of 128 inputs (its buffers of x and codes go round every two or
-three) and over chunks of one to six tiles of 32 rows.  Formula and tolerance as in test_gpu_int4_linear."""
+three) and over chunks of one to six tiles of 32 rows, and calls in flight at
+the same time.  Formula and tolerance as in test_gpu_int4_linear."""
 import pytest
 import torch
 
@@ -93,3 +94,46 @@ def test_many_rows_past_4_gib():
     pick = torch.arange(0, N, 97, device="cuda")
     want, tol = formula(x, packed[E - 1][pick], scales[E - 1][pick], G, "none")
     check(out[:, pick], want, tol, torch.float32, f"{rows} rows")
+
+
+def in_flight(calls):
+    """Each of `calls`, five times on a stream of its own, against what it answers alone."""
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = []
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((i, calls[i]()))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i, y in got)
+
+
+def test_one_layer_on_two_streams():
+    """Calls of one layer in flight at the same time, whose workspaces must not be one: the copy of x differs."""
+    T, N, K = 512, 6000, 1280
+    g = generator(61)
+    layer = Int4Linear(*weights((N,), K, 128, g), 128)
+    assert copies_x(B.moe_int4_linear_workspace_bytes(T, N, K, 128), T, K)
+    xs = [torch.randn(T, K, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2)]
+    in_flight([lambda x=x: layer.forward(x, out_dtype=torch.float32) for x in xs])
+
+
+@pytest.mark.parametrize("P,N", [(300, 1000), (1500, 1700)])
+def test_one_set_of_experts_on_two_streams(P, N):
+    """The same with experts, by the list of tiles and by the copy of x; the two calls' offsets differ."""
+    E, K = 11, 640
+    g = generator(67)
+    layer = Int4GroupedLinear(*weights((E, N), K, 128, g), 128)
+    x = torch.randn(P, K, device="cuda", generator=g).to(torch.bfloat16)
+    offs = []
+    for seed in range(2):
+        ids = (torch.rand(P, device="cuda", generator=generator(seed)) ** 2 * E).long()
+        off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+        off[1:] = torch.cumsum(torch.bincount(ids, minlength=E), 0)
+        offs.append(off)
+    groups = B.make_groups(P, P, P, offs[0])
+    need = B.moe_int4_grouped_linear_workspace_bytes(groups, N, K, 128)
+    assert need > 0 and copies_x(need, P, K) == (P == 1500)
+    in_flight([lambda o=o: layer.forward(x, o, out_dtype=torch.float32) for o in offs])
