@@ -851,7 +851,8 @@ static int32_t int4_sizes(const moe_int4_groups *g, int32_t tokens, int32_t n, i
     if ((rc = check_int4_rows("places", g->places, n)) || (rc = check_int4_rows("out_rows", g->out_rows, n)) ||
         (rc = check_int4_rows("x_rows", g->x_rows, k)) || (rc = check_int4_rows("places", g->places, kp, 1)))
         return rc;
-    // fewer than 2^32 threads in one launch: a workgroup takes 16 rows of an expert and 64 columns
+    // fewer than 2^32 threads in one launch: two for a column of at most places / 16 + min(experts, places)
+    // tiles.  (Few places take a workgroup each instead where that stays below, too.)
     if ((long long)(g->experts < g->places ? g->experts : g->places) * n >= (1LL << 29))
         return fail(MOE_INT4_EINVAL, "min(experts, places) * n must stay below 2^29");
     if (g->gather && g->gather_div < 1) return fail(MOE_INT4_EINVAL, "gather_div=%d must be positive", g->gather_div);

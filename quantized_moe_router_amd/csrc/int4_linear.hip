@@ -870,8 +870,13 @@ bool many_rows(const Int4Args &a)
 {
     return a.places >= 32L * a.experts && (long)((a.places + 127) / 128) * ((a.N + 255) / 256) >= 80;
 }
-// Few places: the workgroups find their experts themselves.
-bool listed(const Int4Args &a) { return a.offsets && a.places > 128; }
+// Few places: the workgroups find their experts themselves, 256 threads for each
+// place and 128 columns.  Where these would be 2^32 (of 2^24 columns) the list,
+// which has a tile for every sixteen places and expert, stays below.
+bool listed(const Int4Args &a)
+{
+    return a.offsets && (a.places > 128 || (long)a.places * ((a.N + 127) / 128) >= 1L << 24);
+}
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 

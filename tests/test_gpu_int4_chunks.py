@@ -137,3 +137,23 @@ def test_one_set_of_experts_on_two_streams(P, N):
     need = B.moe_int4_grouped_linear_workspace_bytes(groups, N, K, 128)
     assert need > 0 and copies_x(need, P, K) == (P == 1500)
     in_flight([lambda o=o: layer.forward(x, o, out_dtype=torch.float32) for o in offs])
+
+
+def test_few_places_of_the_widest_matrix():
+    """128 places of 2^24 - 1 columns, 2^31 - 128 elements of out."""
+    E, P, N, K, G = 5, 128, (1 << 24) - 1, 64, 64
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GiB of GPU memory")
+    g = generator(71)
+    packed, scales = weights((E, N), K, G, g)
+    x = torch.randn(P, K, device="cuda", generator=g).to(torch.bfloat16)
+    off = torch.tensor([0, 100, 100, 100, 101, P], dtype=torch.int32, device="cuda")
+    out = torch.full((P, N), 77.0, dtype=torch.bfloat16, device="cuda")
+    Int4GroupedLinear(packed, scales, G).forward(x, off, out=out)
+    pick = torch.cat([torch.arange(200, device="cuda"), torch.arange(1000, N, 100003, device="cuda"),
+                      torch.arange(N - 200, N, device="cuda")])
+    for e, a, b in ((0, 0, 100), (3, 100, 101), (4, 101, P)):
+        want, tol = formula(x[a:b], packed[e][pick], scales[e][pick], G, "none")
+        check(out[a:b][:, pick], want, tol, torch.bfloat16, f"expert {e}")
+    for a in range(0, P, 16):   # every element has been written: no product is near the fill
+        assert (out[a:a + 16] == 77.0).sum() == 0
