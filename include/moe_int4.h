@@ -472,7 +472,8 @@ typedef struct moe_int4_groups {
  * 128) below 2^31, with gather x_rows * x_stride too; min(experts, places) *
  * n below 2^29; places = 0 is a no-op.  Without gather x has
  * at least places rows, without scatter so has out; a residual that is out
- * itself needs scatter to name no row twice.  Otherwise as moe_int4_linear. */
+ * itself needs scatter to name no row twice.  Otherwise as moe_int4_linear.
+ * The query reads the sizes of `groups` alone: its tables may still be NULL. */
 int32_t moe_int4_grouped_linear_workspace_bytes(const moe_int4_groups *groups, int32_t n,
                                                 int32_t k, int32_t group, size_t *bytes);
 int32_t moe_int4_grouped_linear(const uint16_t *x, int64_t x_stride, const int32_t *w_packed,

@@ -828,7 +828,8 @@ static int32_t check_int4_rows(const char *name, int32_t rows, int32_t cols, int
     return MOE_INT4_OK;
 }
 
-// The sizes of a call, from which its plan and workspace follow.
+// The sizes of a call, from which its plan and workspace follow.  A query of the
+// workspace may come before the tables are there: nothing here depends on them.
 static int32_t int4_sizes(const moe_int4_groups *g, int32_t tokens, int32_t n, int32_t k, int32_t group, Int4Args *a)
 {
     int32_t rc = check_int4_matrix(n, k, group);
@@ -855,15 +856,23 @@ static int32_t int4_sizes(const moe_int4_groups *g, int32_t tokens, int32_t n, i
     // tiles.  (Few places take a workgroup each instead where that stays below, too.)
     if ((long long)(g->experts < g->places ? g->experts : g->places) * n >= (1LL << 29))
         return fail(MOE_INT4_EINVAL, "min(experts, places) * n must stay below 2^29");
+    a->grouped = true;
+    a->experts = g->experts;
+    a->places = g->places;
+    a->x_rows = g->x_rows;
+    a->out_rows = g->out_rows;
+    return MOE_INT4_OK;
+}
+
+// The tables of a grouped call, and whether its operands have the rows that it needs with them.
+static int32_t int4_tables(const moe_int4_groups *g, Int4Args *a)
+{
+    if (g->places > 0 && !g->offsets) return fail(MOE_INT4_EINVAL, "offsets is NULL");
     if (g->gather && g->gather_div < 1) return fail(MOE_INT4_EINVAL, "gather_div=%d must be positive", g->gather_div);
     if (g->places > 0 && g->x_rows < (g->gather ? 1 : g->places))
         return fail(MOE_INT4_EINVAL, "x_rows=%d, %d places need %d", g->x_rows, g->places, g->gather ? 1 : g->places);
     if (g->places > 0 && g->out_rows < (g->scatter ? 1 : g->places))
         return fail(MOE_INT4_EINVAL, "out_rows=%d, %d places need %d", g->out_rows, g->places, g->scatter ? 1 : g->places);
-    a->experts = g->experts;
-    a->places = g->places;
-    a->x_rows = g->x_rows;
-    a->out_rows = g->out_rows;
     if (g->gather) a->gather_div = g->gather_div;
     a->offsets = g->offsets;
     a->gather = g->gather;
@@ -977,8 +986,7 @@ int32_t moe_int4_grouped_linear(const uint16_t *x, int64_t x_stride, const int32
     if (!groups) return fail(MOE_INT4_EINVAL, "groups is NULL");
     Int4Args a;
     int32_t rc = int4_sizes(groups, 0, n, k, group, &a);
-    if (rc) return rc;
-    if (a.places > 0 && !a.offsets) return fail(MOE_INT4_EINVAL, "offsets is NULL");
+    if (rc || (rc = int4_tables(groups, &a))) return rc;
     return int4_call(a, x, x_stride, w_packed, w_scales, epilogue, out, out_type, out_stride, workspace,
                      workspace_bytes, (hipStream_t)hip_stream);
 }

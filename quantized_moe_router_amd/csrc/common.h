@@ -636,6 +636,7 @@ struct Int4Args {
     int N, K, G;
     int places;              // rows of the sorted order (tokens, without tables)
     int experts, x_rows, out_rows, gather_div;
+    bool grouped;            // places sorted by expert; plan and workspace follow from it, not from offsets
     const int32_t *offsets;  // null: every place belongs to the one matrix, and places are rows
     const int32_t *gather, *scatter;
     const float *row_weights;

@@ -857,7 +857,7 @@ void launch_rows(const Int4Args &a, const Int4Tiles &tl, hipStream_t st)
 // Most tiles of `most` rows that the places can make.
 int most_tiles(const Int4Args &a, int most)
 {
-    if (!a.offsets) return (a.places + most - 1) / most;
+    if (!a.grouped) return (a.places + most - 1) / most;
     return a.places / most + (a.experts < a.places ? a.experts : a.places);
 }
 
@@ -875,7 +875,7 @@ bool many_rows(const Int4Args &a)
 // which has a tile for every sixteen places and expert, stays below.
 bool listed(const Int4Args &a)
 {
-    return a.offsets && (a.places > 128 || (long)a.places * ((a.N + 127) / 128) >= 1L << 24);
+    return a.grouped && (a.places > 128 || (long)a.places * ((a.N + 127) / 128) >= 1L << 24);
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -889,7 +889,7 @@ Int4Plan tile_plan(const Int4Args &a)
     // 192 rows where the experts have more than 96 each (81920 places of 512
     // experts 704 us, with 128 rows 730), 128 otherwise (20480 places 330, 347;
     // 512 tokens of one matrix 49, 62: the last round of tiles fills the chip better)
-    p.most = a.offsets && a.places > 96L * a.experts ? 192 : 128;
+    p.most = a.grouped && a.places > 96L * a.experts ? 192 : 128;
     p.tiles = most_tiles(a, p.most);
     p.exps_at = up256(2 * (size_t)(p.rows + 1) * p.kp);
     p.list_at = p.exps_at + up256(4 * (size_t)(p.rows + 1));
@@ -914,7 +914,7 @@ hipError_t launch_int4_linear(const Int4Args &a, void *workspace, hipStream_t st
         uint16_t *xp = reinterpret_cast<uint16_t *>(ws);
         int *exps = reinterpret_cast<int *>(ws + pl.exps_at);
         int4 *list = reinterpret_cast<int4 *>(ws + pl.list_at);
-        int4_prepare_kernel<<<(pl.rows + 4) / 4 + (a.offsets ? 1 : 0), 256, 0, st>>>(a, pl, xp, exps, list);
+        int4_prepare_kernel<<<(pl.rows + 4) / 4 + (a.grouped ? 1 : 0), 256, 0, st>>>(a, pl, xp, exps, list);
         if (a.G == 128) pl.most == 192 ? launch_tiles<128, 6>(a, pl, xp, exps, list, st) : launch_tiles<128, 4>(a, pl, xp, exps, list, st);
         else pl.most == 192 ? launch_tiles<64, 6>(a, pl, xp, exps, list, st) : launch_tiles<64, 4>(a, pl, xp, exps, list, st);
         return hipGetLastError();
@@ -926,7 +926,7 @@ hipError_t launch_int4_linear(const Int4Args &a, void *workspace, hipStream_t st
         int4_list_kernel<<<1, 256, 0, st>>>(a, 16, tl.count, list);
         tl.list = list;
     } else {
-        tl.count = a.offsets ? a.places : (a.places + 15) / 16;
+        tl.count = a.grouped ? a.places : (a.places + 15) / 16;
     }
     // Enough columns to go round: the waves of a workgroup take columns and share
     // x (640 places of 512 experts, [2560, 640]: 70 us, with K over the waves
@@ -935,7 +935,7 @@ hipError_t launch_int4_linear(const Int4Args &a, void *workspace, hipStream_t st
     // 16.8, 21.6 and 18.7).  A long K of few columns takes eight, where columns
     // are very few with one column tile a wave (16 tokens of [5120, 5120] 8.1 us
     // against 9.5 with four; 32 of [33, 10240] 8.3, 14.3).
-    const bool four = !a.offsets && a.places <= 4;
+    const bool four = !a.grouped && a.places <= 4;
     const long columns = (long)tl.count * ((a.N + 31) / 32);
     if (columns >= 2048) four ? launch_rows<2, 1, 4, 4>(a, tl, st) : launch_rows<2, 1, 4, 16>(a, tl, st);
     else if (a.K >= 4096 && columns <= 64) four ? launch_rows<1, 8, 1, 4>(a, tl, st) : launch_rows<1, 8, 1, 16>(a, tl, st);
