@@ -17,18 +17,15 @@ namespace {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-// Global memory straight into LDS: lane l's BYTES from `at` + `more` bytes into
-// a buffer go to `to` + l BYTES, `more` and `to` the same for the whole wave.
-// The wave waits for them with wait_loads.  (By buffer, for the compiler takes
-// the form with a pointer for one that may be out of order among the loads, and
-// waits for all of them where it needs one.)
+// Global memory straight into LDS: lane l's 16 bytes from `at` + `more` bytes
+// into a buffer go to `to` + 16 l bytes, `more` and `to` the same for the whole
+// wave.  The wave waits for them with wait_loads.  (By buffer, for the compiler
+// takes the form with a pointer for one that may be out of order among the
+// loads, and waits for all of them where it needs one.)
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
-template <int BYTES>
 __device__ __forceinline__ void load_to_lds(rsrc_t from, uint32_t at, uint32_t more, void *to)
 {
-    auto *t = (__attribute__((address_space(3))) void *)to;
-    if constexpr (BYTES == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(from, t, 16, at, more, 0, 0);
-    else __builtin_amdgcn_raw_ptr_buffer_load_lds(from, t, 4, at, more, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 16, at, more, 0, 0);
 }
 __device__ __forceinline__ rsrc_t buffer_of(const void *p, uint32_t bytes)
 {
@@ -298,10 +295,10 @@ __global__ __launch_bounds__(KS * WC * kWave) void int4_rows_kernel(Int4Args g, 
     }
     auto copy = [&](int u, int buf) __attribute__((always_inline)) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) load_to_lds<16>(w_buf, wsrc + (uint32_t)(64 * t) * (uint32_t)kw, 64 * u, s.w[wave][buf] + t * 256);
+        for (int t = 0; t < NT; ++t) load_to_lds(w_buf, wsrc + (uint32_t)(64 * t) * (uint32_t)kw, 64 * u, s.w[wave][buf] + t * 256);
 #pragma unroll
         for (int i = 0; i < kXCopies; ++i)   // (half a unit at K's end: what comes behind it is not used)
-            load_to_lds<16>(x_buf, xsrc[i], 256 * u, s.x[ks][buf] + copied(i) * 512);
+            load_to_lds(x_buf, xsrc[i], 256 * u, s.x[ks][buf] + copied(i) * 512);
     };
     // scales of kAhead units, a lane a row
     auto scales = [&](int u) __attribute__((always_inline)) {
@@ -625,7 +622,7 @@ __global__ __launch_bounds__(WAVES * kWave) void int4_tile_kernel(Int4Args g, In
         wsrc[o] = 4u * (uint32_t)(32 * wave + row) * (uint32_t)kw + 16 * ((lane & 3) ^ (row >> 2 & 3));
     }
     auto copy_w = [&](int st, int buf, int o) __attribute__((always_inline)) {
-        load_to_lds<16>(w_buf, wsrc[o], kStageK / 2 * min(st, stages - 1), s.w[buf] + (32 * wave + 16 * o) * (kStageK / 8));
+        load_to_lds(w_buf, wsrc[o], kStageK / 2 * min(st, stages - 1), s.w[buf] + (32 * wave + 16 * o) * (kStageK / 8));
     };
 #pragma unroll
     for (int o = 0; o < 4; ++o) copy_w(o >> 1, o >> 1, o & 1);
@@ -653,7 +650,7 @@ __global__ __launch_bounds__(WAVES * kWave) void int4_tile_kernel(Int4Args g, In
         src[o] = 2u * (uint32_t)s.row[row] * (uint32_t)pl.kp + 16 * ((lane & 15) ^ (row & 15));
     }
     auto copy_x = [&](int st, int buf, int o) __attribute__((always_inline)) {
-        load_to_lds<16>(x_buf, src[o], 2 * kStageK * min(st, stages - 1), s.x[buf] + 4 * (WAVES * o + wave) * kStageK);
+        load_to_lds(x_buf, src[o], 2 * kStageK * min(st, stages - 1), s.x[buf] + 4 * (WAVES * o + wave) * kStageK);
     };
 #pragma unroll
     for (int o = 0; o < kX; ++o) copy_x(0, 0, o);
@@ -786,13 +783,14 @@ __global__ __launch_bounds__(WAVES * kWave) void int4_tile_kernel(Int4Args g, In
             }
         }
     };
-    switch (mtiles) {
-    case 1: all(std::integral_constant<int, 1>{}); break;
-    case 2: all(std::integral_constant<int, 2 < MAXMA ? 2 : MAXMA>{}); break;
-    case 3: all(std::integral_constant<int, 3 < MAXMA ? 3 : MAXMA>{}); break;
-    case 4: all(std::integral_constant<int, 4 < MAXMA ? 4 : MAXMA>{}); break;
-    case 5: all(std::integral_constant<int, 5 < MAXMA ? 5 : MAXMA>{}); break;
-    default: all(std::integral_constant<int, MAXMA>{}); break;
+    static_assert(MAXMA == 4 || MAXMA == 6, "a case for each number of row tiles");
+    if (mtiles == 1) all(std::integral_constant<int, 1>{});
+    else if (mtiles == 2) all(std::integral_constant<int, 2>{});
+    else if (mtiles == 3) all(std::integral_constant<int, 3>{});
+    else if (MAXMA == 4 || mtiles == 4) all(std::integral_constant<int, 4>{});
+    else if constexpr (MAXMA == 6) {
+        if (mtiles == 5) all(std::integral_constant<int, 5>{});
+        else all(std::integral_constant<int, 6>{});
     }
     wait_loads<0>();   // the copies of stages that do not come, too
 

@@ -78,14 +78,6 @@ __device__ __forceinline__ double term(float l, float top)
     return exp_below((double)l - (double)top);
 }
 
-__device__ __forceinline__ void larger(float &top, int &at, float other, int place)
-{
-    if (other > top || (other == top && place < at)) {
-        top = other;
-        at = place;
-    }
-}
-
 // Sum over the wave, the same for every lane, in a fixed order.
 template <int CTRL>
 __device__ __forceinline__ double dpp_move64(double v)

@@ -44,8 +44,10 @@ def test_order_of_a_stage(kernels, group, tiles):
     in_flight = copies_x + 2 + 2 * scales if deep else 2 + scales
     codes = next(m[1] for m in map(COPY.search, lines) if m)   # the first copies are of codes
     stages, stage = [], None
-    for line in lines:
-        if f"s_waitcnt vmcnt({in_flight}) lgkmcnt(0)" in line:
+    lines = [l for l in lines if l.strip() and not l.strip().startswith((";", "."))]
+    for line, behind in zip(lines, lines[1:]):
+        # a stage's own wait and its barrier (the compiler's waits elsewhere may have the same count)
+        if f"s_waitcnt vmcnt({in_flight}) lgkmcnt(0)" in line and "s_barrier" in behind:
             stage = []
             stages.append(stage)
         elif stage is not None and len(stage) < copies_x + 2 + scales:
