@@ -410,19 +410,24 @@ int32_t moe_int4_logits_process(const void *logits, int32_t logits_type, int64_t
  *             what lies between the rows is left as it was
  *   epilogue  may be NULL (out is then the plain product)
  * Numerics: neither x nor a weight is rounded to fewer bits where it counts.
- * With few rows (below 32 to an expert always) products are formed as x * (code + 24) less
- * 24 * x, exactly, and summed in fp32 group by group; values of x beyond 2^110
- * may overflow on the way.  With many rows x and code * scale are taken as fp16
- * values times a power of two of their own row: exact but for inputs below
- * 2^-28 and scales below 2^-24 of the largest of their row, which are off by at
- * most 2^-38 (x) and 2^-35 (scales) of that largest.  Subnormal values of x and
- * of the scales may count as zero.  Either way a token with an
- * infinity or a NaN in x has NaN in all its own products, and in no others; an
- * infinite or NaN scale makes its row's outputs NaN or infinite.
+ * With few rows (below 32 to an expert always) products are formed as
+ * x * (code + 24) less 24 * x, exactly, and summed in fp32 group by group, so
+ * that the sums pass through values of up to 24 times a group's sum of |x|,
+ * whose roundings remain: an output is off by about 10^-7 of its size (2-norm;
+ * a plain fp32 sum by 0.5 to 2.5 10^-7), with x of one sign by up to 10^-6.
+ * Values of x beyond 2^110 may overflow on the way.  With many rows x and
+ * code * scale are taken as fp16 values times a power of two of their own row:
+ * exact but for inputs below 2^-28 and scales below 2^-24 of the largest of
+ * their row, which are off by at most 2^-38 (x) and 2^-35 (scales) of that
+ * largest.  Subnormal values of x and of the scales may count as zero.  Either
+ * way a token with an infinity or a NaN in x has NaN in all its own products,
+ * and in no others; an infinite or NaN scale makes its row's outputs NaN or
+ * infinite (for a row of x that counts as zeros they may be zero instead).
  * group is 64 or 128, k a multiple of it (at most 65536), n in [1, 2^24],
  * tokens in [0, 2^20] with tokens * n and (tokens + 1) * (k rounded up to a
- * multiple of 128) below 2^31; tokens = 0 is a no-op.  Strides, alignment, overlaps, workspace and streams as in
- * moe_int8_linear_fused.  The result does not depend on timing. */
+ * multiple of 128) below 2^31; tokens = 0 is a no-op.  Strides, alignment,
+ * overlaps, workspace and streams as in moe_int8_linear_fused.  The result does
+ * not depend on timing. */
 int32_t moe_int4_linear_workspace_bytes(int32_t tokens, int32_t n, int32_t k, int32_t group,
                                         size_t *bytes);
 int32_t moe_int4_linear(const uint16_t *x, int64_t x_stride, const int32_t *w_packed,

@@ -204,14 +204,22 @@ struct Int4Tiles {
 // matrix cores: the accumulators of a group begin at the product of x with a
 // matrix of -24 (one such product serves every column tile of the wave), and
 // what the group's products leave there is sum x code, exact up to fp32's
-// additions.  The group's scale multiplies that sum in fp32, so neither x nor
-// a weight is ever rounded.
+// additions.  These pass through 24 sum |x| of a group: for x of one sign an
+// output is off by up to 1.0e-6 of its size (a plain fp32 sum 2e-7), for x of
+// both signs by 1.2e-7 (2.6e-7; K of 2560, groups of 128).  The group's scale
+// multiplies that sum in fp32, so neither x nor a weight is ever rounded.  (The
+// 24 taken off after every 32 inputs, in each column tile: 2.3e-7 for x of one
+// sign, and 1 to 3.5 % more time, 216 -> 218 us for 5120 places, 27.1 -> 28.1
+// for 128 tokens of [10240, 2560].)
 //
-// What bounds it: memory where it is large (one token of [248320, 2560] 70 us,
-// 4.7 TB/s, the rate of a copy; 5120 places of 512 experts, [1280, 2560], 215 us,
-// 4.1 TB/s, with the vector ALU busy 55 % of the time), and the way through
-// its dependent loads where it is small (one token of [2560, 2560]: 6 us, of
-// which the matrix takes 0.7).  Straight to LDS against loads into registers in
+// What bounds it: memory where it is large (one token of [248320, 2560] 72 us,
+// 4.6 TB/s, nearly the rate of a copy; 5120 places of 512 experts, [1280, 2560],
+// 216 us, 4.1 TB/s, with the vector ALU busy 55 % of the time), and the way
+// through its dependent loads where it is small (one token of [2560, 2560]: 6
+// us, of which the matrix takes 0.7).  Between them, 17 to 512 rows of a matrix
+// (64 tokens of [10240, 2560] 17 us, where memory takes 3), it makes the codes
+// anew for every 16 rows.  The buffer of the codes is held in vector registers
+// (for the clamp of its rows), so each copy of codes is a loop over it.  Straight to LDS against loads into registers in
 // the operands' order: 70 us against 82, and 12.6 against 15.0 for 32 tokens of
 // [10240, 2560] (10.9 with two column tiles a wave).
 template <int G, int NT, int KS, int WC, int XR>
@@ -432,13 +440,17 @@ __global__ __launch_bounds__(KS * WC * kWave) void int4_rows_kernel(Int4Args g, 
 // row, cost more here than the three instructions a word more do (81920 places
 // of 512 experts, [1280, 2560]: 820 us against 749).
 //
-// What bounds it: at 81920 places (690 us, 778 TFLOP/s, 62 % of a large library
-// product) the matrix cores are busy 42 % of the cycles, the vector ALU 27 %, LDS
-// 25 %; waves wait two fifths of their time, most of it where a stage begins:
-// a barrier, the first reads of LDS and the first weights follow each other
-// (about 1300 cycles of a stage's 3400 with 128 rows; a row tile more costs what
-// its products cost).  512 tokens of [10240, 2560] (49 us): 160 workgroups for 256
-// CUs besides, and 11 us of the pass over x, the start and the end.
+// What bounds it: at 81920 places (690 to 708 us, 758 to 778 TFLOP/s, 62 % of a
+// large library product) the matrix cores are busy 45 % of the cycles, the vector
+// ALU 26 %, LDS 27 %; waves wait two fifths of their time, most of it where a
+// stage begins: a barrier, the first reads of LDS and the first weights follow
+// each other (about 1300 cycles of a stage's 3400 with 128 rows; a row tile more
+// costs what its products cost).  Part of that is that the scales cross the loop
+// in registers: where a turn of the loop begins (three stages; of chunks of 192
+// six, and there in the second stage, too) the compiler waits for every load
+// before it reads them, the copies for the next stages among them.  512 tokens of
+// [10240, 2560] (49 us): 160 workgroups for 256 CUs besides, and 11 us of the
+// pass over x, the start and the end.
 // ---------------------------------------------------------------------------
 constexpr int kStageK = 128;
 
@@ -861,9 +873,9 @@ int most_tiles(const Int4Args &a, int most)
 
 // Whether the rows are many enough for the kernel that makes a copy of x: a
 // third of the chip's CUs with a tile of 128 x 256 (512 tokens of [10240, 2560]
-// 48 us, by sixteen rows 81; 256 tokens 41 and 43; of [2560, 2560], 512 tokens
-// 43 and 26), and 32 rows to an expert (20480 places of 512 experts 333 us
-// against 458, 10240 places, which stay with the other, 279).
+// 49 us, by sixteen rows 81; 256 tokens 40 and 43; 128 tokens, which stay with
+// the other, 39 and 27; of [2560, 2560], 512 tokens 41 and 25), and 32 rows to an
+// expert (20480 places of 512 experts 334 us against 455; 10240 places 288, 278).
 bool many_rows(const Int4Args &a)
 {
     return a.places >= 32L * a.experts && (long)((a.places + 127) / 128) * ((a.N + 255) / 256) >= 80;
@@ -885,8 +897,8 @@ Int4Plan tile_plan(const Int4Args &a)
     p.rows = p.by_place ? a.places : a.x_rows;
     p.kp = (a.K + kStageK - 1) / kStageK * kStageK;
     // 192 rows where the experts have more than 96 each (81920 places of 512
-    // experts 704 us, with 128 rows 730), 128 otherwise (20480 places 330, 347;
-    // 512 tokens of one matrix 49, 62: the last round of tiles fills the chip better)
+    // experts 706 us, with 128 rows 738), 128 otherwise (20480 places 334, 348;
+    // 512 tokens of one matrix 49, 63: the last round of tiles fills the chip better)
     p.most = a.grouped && a.places > 96L * a.experts ? 192 : 128;
     p.tiles = most_tiles(a, p.most);
     p.exps_at = up256(2 * (size_t)(p.rows + 1) * p.kp);
@@ -927,12 +939,13 @@ hipError_t launch_int4_linear(const Int4Args &a, void *workspace, hipStream_t st
         tl.count = a.grouped ? a.places : (a.places + 15) / 16;
     }
     // Enough columns to go round: the waves of a workgroup take columns and share
-    // x (640 places of 512 experts, [2560, 640]: 70 us, with K over the waves
-    // 118).  Fewer: four of them share K (8 tokens of [10240, 2560] 7.8 us, with
-    // columns over the waves 15.9, with four column tiles a wave 8.2; 64 tokens
-    // 16.8, 21.6 and 18.7).  A long K of few columns takes eight, where columns
-    // are very few with one column tile a wave (16 tokens of [5120, 5120] 8.1 us
-    // against 9.5 with four; 32 of [33, 10240] 8.3, 14.3).
+    // x (640 places of 512 experts, [2560, 640]: 71 us, with K over the waves 141,
+    // with that and four column tiles a wave 119).  Fewer: four of them share K (8
+    // tokens of [10240, 2560] 8.0 us, with columns over the waves 15.7, with four
+    // column tiles a wave 8.5; 64 tokens 16.8, 21.0 and 18.9).  A long K of few
+    // columns takes eight, where columns are very few with one column tile a wave
+    // (16 tokens of [5120, 5120] 8.3 us against 9.7 with four; 32 of [33, 10240]
+    // 8.5, 14.5).
     const bool four = !a.grouped && a.places <= 4;
     const long columns = (long)tl.count * ((a.N + 31) / 32);
     if (columns >= 2048) four ? launch_rows<2, 1, 4, 4>(a, tl, st) : launch_rows<2, 1, 4, 16>(a, tl, st);
