@@ -440,7 +440,7 @@ __global__ __launch_bounds__(KS * WC * kWave) void int4_rows_kernel(Int4Args g, 
 // row, cost more here than the three instructions a word more do (81920 places
 // of 512 experts, [1280, 2560]: 820 us against 749).
 //
-// What bounds it: at 81920 places (690 to 708 us, 758 to 778 TFLOP/s, 62 % of a
+// What bounds it: at 81920 places (684 to 708 us, 758 to 785 TFLOP/s, 61 % of a
 // large library product) the matrix cores are busy 45 % of the cycles, the vector
 // ALU 26 %, LDS 27 %; waves wait two fifths of their time, most of it where a
 // stage begins: a barrier, the first reads of LDS and the first weights follow

@@ -17,12 +17,12 @@
 // fp32's error of some border about once in a hundred.
 //
 // What bounds it: 64 sequences with three drafts over 248320 tokens (fp32) take
-// 108 us.  One by one, under a profiler, which parts the launches, the first takes
-// 75 (the rows' bytes at the rate of a copy, with the vector ALU busy 70 % of the
-// time), the second 30, of which half goes by before a workgroup has its
-// sequence's decision, made anew by each of them from a few hundred slabs, and the
-// third 11.  One sequence takes 20, so parted 6, 5 and 5 to 8, dependent loads all
-// of them; 8 sequences 40, where the bytes take 9: three launches and the
+// 106 to 112 us.  One by one, under a profiler, which parts the launches, the
+// first takes 75 (the rows' bytes at the rate of a copy, with the vector ALU busy
+// 70 % of the time), the second 30, of which half goes by before a workgroup has
+// its sequence's decision, made anew by each of them from a few hundred slabs, and
+// the third 11.  One sequence takes 20, so parted 6, 5 and 5 to 8, dependent loads
+// all of them; 8 sequences 40, where the bytes take 9: three launches and the
 // decisions.  Rows that do not begin on a word of four tokens, and the last slab
 // of every row, are loaded token by token (33 sequences of 16-bit rows: 33 us,
 // where the bytes take 4).  Every slab's workgroup deciding for itself saves a
