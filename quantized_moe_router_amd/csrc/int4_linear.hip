@@ -219,9 +219,10 @@ struct Int4Tiles {
 // us, of which the matrix takes 0.7).  Between them, 17 to 512 rows of a matrix
 // (64 tokens of [10240, 2560] 17 us, where memory takes 3), it makes the codes
 // anew for every 16 rows.  The buffer of the codes is held in vector registers
-// (for the clamp of its rows), so each copy of codes is a loop over it.  Straight to LDS against loads into registers in
-// the operands' order: 70 us against 82, and 12.6 against 15.0 for 32 tokens of
-// [10240, 2560] (10.9 with two column tiles a wave).
+// (for the clamp of its rows), so each copy of codes is a loop over it.  Straight
+// to LDS against loads into registers in the operands' order: 70 us against 82,
+// and 12.6 against 15.0 for 32 tokens of [10240, 2560] (11.1 with two column tiles
+// a wave).
 template <int G, int NT, int KS, int WC, int XR>
 __global__ __launch_bounds__(KS * WC * kWave) void int4_rows_kernel(Int4Args g, Int4Tiles tl, int nblocks)
 {
